@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(_HERE, "libeffort.so")
 # -DEFFORT_DEBUG report bad indices through effort_check instead of using them)
 LIB_DEBUG_PATH = os.path.join(_HERE, "libeffort_debug.so")
 
-F32, F16 = 0, 1
+F32, F16, BF16 = 0, 1, 2
 STATUS = {0: "ok", 1: "invalid argument", 2: "CUDA error", 3: "out of memory",
           4: "non-finite input", 5: "device-side inconsistency", 6: "unsupported size"}
 MAX_OUT_DIM = 32768
@@ -77,6 +77,18 @@ def lib():
             "effort_last_call_bytes": [vp, ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_uint64)],
             "effort_workspace_last_call_bytes": [vp, ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_uint64)],
             "effort_workspace_check": [vp],
+            "effort_block_norm": [vp, vp],
+            "effort_fp8_prepare": [vp, vp, i64, i64, vp, ctypes.POINTER(vp)],
+            "effort_fp8_matmul": [vp, vp, i64, vp, i64, i64, ctypes.c_int, vp, i64, vp],
+            "effort_fp8_get_info": [vp, ctypes.POINTER(i64), ctypes.POINTER(i64), ctypes.POINTER(ctypes.c_size_t)],
+            "effort_fp8_destroy": [vp],
+            "effort_moe_prepare": [vp, vp, ctypes.POINTER(vp)],
+            "effort_moe_scratch_bytes": [vp, i64, i32, ctypes.POINTER(ctypes.c_size_t)],
+            "effort_moe_forward": [vp, vp, ctypes.c_int, i64, i64, i32, ctypes.c_int, vp, vp, vp, ctypes.c_int, i64,
+                                   vp, ctypes.c_size_t, vp],
+            "effort_moe_get_info": [vp, ctypes.POINTER(i32), ctypes.POINTER(i64), ctypes.POINTER(i64),
+                                    ctypes.POINTER(ctypes.c_size_t)],
+            "effort_moe_destroy": [vp],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -360,3 +372,6 @@ def dense_gemv(ws, W, v, out=None):
     _check(lib().effort_dense_gemv(ws._h, _ptr(W), W.shape[0], W.shape[1], _ptr(v), _vdtype(v), _ptr(out),
                                    _stream(W.device)), "effort_dense_gemv")
     return out
+
+
+from .ffn import BlockNorm, Fp8Matrix, MoeLayer, block_norm, quantize_e4m3  # noqa: E402,F401

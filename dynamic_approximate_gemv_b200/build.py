@@ -4,6 +4,7 @@ Run as ``python -m dynamic_approximate_gemv_b200.build``; ``__graft_entry__``
 calls :func:`build`.  Device code is compiled without fast-math and with
 denormals kept, so the selection products round exactly as the C ABI states.
 """
+import concurrent.futures
 import os
 import subprocess
 import sys
@@ -12,7 +13,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libeffort.so")
 LIB_DEBUG = os.path.join(HERE, "libeffort_debug.so")
-SOURCES = ["api.cu", "prep.cu", "effort.cu", "dense.cu", "noalloc.cu"]
+SOURCES = ["api.cu", "prep.cu", "effort.cu", "dense.cu", "noalloc.cu",
+           "api_ffn.cu", "norm.cu", "fp8.cu", "moe.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = [
@@ -33,16 +35,39 @@ def needs_build():
     return any(os.path.getmtime(p) > t for p in deps if os.path.exists(p))
 
 
-def _compile(out, extra):
-    cmd = [NVCC] + FLAGS + extra + ["-I" + os.path.join(HERE, "..", "include"), "-o", out + ".tmp"] + [
-        os.path.join(CSRC, s) for s in SOURCES]
+def _nvcc(cmd):
     res = subprocess.run(cmd, capture_output=True, text=True)
-    log = res.stdout + res.stderr
-    with open(os.path.join(HERE, "build.log"), "a") as f:
-        f.write(" ".join(cmd) + "\n" + log)
+    log = " ".join(cmd) + "\n" + res.stdout + res.stderr
     if res.returncode != 0:
         raise RuntimeError("nvcc failed:\n" + log[-8000:])
+    return log
+
+
+def _compile(out, extra):
+    """Compiles every source to an object (side by side) and links `out`."""
+    objs = os.path.join(HERE, "_build", os.path.basename(out) + ".o.d")
+    os.makedirs(objs, exist_ok=True)
+    flags = [NVCC] + [f for f in FLAGS if f != "-shared"] + extra + ["-I" + os.path.join(HERE, "..", "include")]
+    pairs = [(os.path.join(CSRC, s), os.path.join(objs, s + ".o")) for s in SOURCES]
+    headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")]
+    headers += [os.path.join(HERE, "..", "include", "effort.h"), __file__]
+    newest = max(os.path.getmtime(h) for h in headers)
+    todo = [(src, o) for src, o in pairs
+            if not os.path.exists(o) or os.path.getmtime(o) < max(newest, os.path.getmtime(src))]
+
+    def one(p):
+        log = _nvcc(flags + ["-c", "-o", p[1] + ".tmp", p[0]])
+        os.replace(p[1] + ".tmp", p[1])
+        return log
+
+    with concurrent.futures.ThreadPoolExecutor(os.cpu_count() or 4) as pool:
+        logs = list(pool.map(one, todo))
+    logs.append(_nvcc([NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", out + ".tmp"]
+                      + [o for _, o in pairs]))
     os.replace(out + ".tmp", out)
+    log = "".join(logs)
+    with open(os.path.join(HERE, "build.log"), "a") as f:
+        f.write(log)
     return log
 
 
@@ -53,6 +78,12 @@ def build(force=False, verbose=False):
     this file."""
     if not force and not needs_build():
         return LIB
+    if force:
+        for lib in (LIB, LIB_DEBUG):
+            for s in SOURCES:
+                o = os.path.join(HERE, "_build", os.path.basename(lib) + ".o.d", s + ".o")
+                if os.path.exists(o):
+                    os.remove(o)
     with open(os.path.join(HERE, "build.log"), "w"):
         pass
     log = _compile(LIB, [])

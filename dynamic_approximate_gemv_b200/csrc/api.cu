@@ -12,6 +12,7 @@
 
 #include "../../include/effort.h"
 #include "effort_internal.cuh"
+#include "host.cuh"
 
 namespace effort {
 cudaError_t launch_prep(const void* W, const uint16_t* scales, int wk, int I, int O, int n, int P, int dstride,
@@ -29,22 +30,21 @@ int dense_ctas_per_sm();
 
 using namespace effort;
 
-namespace {
-
-inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
 // ---------------------------------------------------------------- allocation
 // Every device allocation of the library goes through dev_alloc.  An optional
 // cap on the bytes the library holds at once (environment variable
 // EFFORT_ALLOC_CAP_BYTES) turns larger requests into EFFORT_ERR_NOMEM before
 // CUDA is asked, which lets allocation failure be exercised on purpose.
-std::atomic<unsigned long long> g_live_bytes{0};
+static std::atomic<unsigned long long> g_live_bytes{0};
 
-unsigned long long alloc_cap() {
+static unsigned long long alloc_cap() {
   const char* e = getenv("EFFORT_ALLOC_CAP_BYTES");
   if (!e || !*e) return ~0ull;
   return strtoull(e, nullptr, 10);
 }
+
+namespace effort {
+
 bool within_cap(size_t bytes) { return g_live_bytes.load() + bytes <= alloc_cap(); }
 
 effort_status_t dev_alloc(void** p, size_t bytes) {
@@ -64,19 +64,9 @@ void dev_free(void* p, size_t bytes) {
   g_live_bytes -= bytes;
 }
 
-struct DevBuf {
-  void* p = nullptr;
-  size_t bytes = 0;
-  effort_status_t alloc(size_t b) {
-    bytes = b;
-    return dev_alloc(&p, b);
-  }
-  void release() {
-    dev_free(p, bytes);
-    p = nullptr;
-    bytes = 0;
-  }
-};
+}  // namespace effort
+
+namespace {
 
 // ---------------------------------------------------------------- geometry
 struct Geometry {
@@ -156,17 +146,6 @@ unsigned long long target_count(float effort, long long N) {
 }
 
 bool effort_ok(float e) { return e == e && e > 0.0f && e <= 1.0f; }
-
-struct DeviceGuard {
-  int prev = -1;
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) == cudaSuccess && prev != dev) cudaSetDevice(dev);
-    else prev = -1;
-  }
-  ~DeviceGuard() {
-    if (prev >= 0) cudaSetDevice(prev);
-  }
-};
 
 }  // namespace
 

@@ -1,0 +1,329 @@
+// Host side of the feed-forward operators: argument checks, storage of the
+// weights, and the launches.
+#include <math.h>
+
+#include <new>
+
+#include "../../include/effort.h"
+#include "ffn_common.cuh"
+#include "host.cuh"
+#include "moe.cuh"
+
+namespace effort {
+cudaError_t launch_block_norm(const effort_block_norm_t& a, int sms, cudaStream_t s);
+cudaError_t launch_tile_weights(int wk, const void* w, int mats, int K, int N, uint8_t* out, int cores, int nkb,
+                                size_t stride, int pair, unsigned* status, cudaStream_t s);
+cudaError_t launch_check_finite(const float* p, size_t n, unsigned* status, cudaStream_t s);
+cudaError_t launch_fp8_matmul(const TileMat& w, const float* ws, int I, int O, const uint8_t* x, int64_t xstride,
+                              const float* xs, int64_t xsstride, int64_t rows, int odt, void* out, int64_t ostride,
+                              cudaStream_t s);
+cudaError_t launch_moe(const MoeCall& c, cudaStream_t s);
+size_t moe_scratch_bytes(int n_tokens, int top_k, int F, int wk);
+}  // namespace effort
+
+using namespace effort;
+
+struct effort_fp8_s {
+  int dev = 0;
+  int64_t I = 0, O = 0;
+  DevBuf buf;  // cores, then the scales
+  TileMat w = {};
+  const float* ws = nullptr;
+};
+
+struct effort_moe_s {
+  int dev = 0;
+  int E = 0, wk = 0, rdt = 0;
+  int64_t I = 0, F = 0;
+  DevBuf buf;  // cores of w1/w3, cores of w2, scales, router
+  TileMat w13 = {}, w2 = {};
+  const float *s1 = nullptr, *s3 = nullptr, *s2 = nullptr;
+  const void* router = nullptr;
+};
+
+namespace {
+
+bool dtype_ok(int t) { return t == EFFORT_F32 || t == EFFORT_F16 || t == EFFORT_BF16; }
+size_t dtype_size(int t) { return t == EFFORT_F32 ? 4 : 2; }
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+bool kind_ok(int k) { return k == EFFORT_NORM_NONE || k == EFFORT_NORM_RMS || k == EFFORT_NORM_LAYER; }
+
+effort_status_t device_sms(int* sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return EFFORT_ERR_CUDA;
+  }
+  return EFFORT_OK;
+}
+
+effort_status_t launched(cudaError_t e) {
+  if (e == cudaSuccess) return EFFORT_OK;
+  cudaGetLastError();
+  return EFFORT_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+effort_status_t effort_block_norm(const effort_block_norm_t* args, void* stream) {
+  if (!args) return EFFORT_ERR_ARG;
+  const effort_block_norm_t& a = *args;
+  if (a.rows < 0 || a.dim < 1 || !a.x) return EFFORT_ERR_ARG;
+  if (!dtype_ok(a.dtype) || !dtype_ok(a.weight_dtype) || (a.h_out && !dtype_ok(a.h_dtype))) return EFFORT_ERR_ARG;
+  if (!kind_ok(a.post_kind) || !kind_ok(a.pre_kind)) return EFFORT_ERR_ARG;
+  if (!a.x_out && !a.h_out && !a.q_out) return EFFORT_ERR_ARG;
+  if ((a.q_out != nullptr) != (a.q_scales != nullptr)) return EFFORT_ERR_ARG;
+  // what works on y is not given without it
+  if (!a.y && (a.gate || a.post_kind != EFFORT_NORM_NONE)) return EFFORT_ERR_ARG;
+  if (!(a.eps >= 0.0f) || !isfinite(a.eps) || !isfinite(a.weight_offset) || !isfinite(a.residual_scale) ||
+      !isfinite(a.branch_scale))
+    return EFFORT_ERR_ARG;
+  const size_t sz = dtype_size(a.dtype), wsz = dtype_size(a.weight_dtype);
+  if (!aligned(a.x, sz) || !aligned(a.y, sz) || !aligned(a.gate, sz) || !aligned(a.x_out, sz)) return EFFORT_ERR_ARG;
+  if (!aligned(a.post_weight, wsz) || !aligned(a.post_bias, wsz) || !aligned(a.pre_weight, wsz) ||
+      !aligned(a.pre_bias, wsz))
+    return EFFORT_ERR_ARG;
+  if (a.h_out && !aligned(a.h_out, dtype_size(a.h_dtype))) return EFFORT_ERR_ARG;
+  if (!aligned(a.q_scales, 4)) return EFFORT_ERR_ARG;
+  if (a.x_stride < a.dim || (a.y && a.y_stride < a.dim) || (a.x_out && a.x_out_stride < a.dim) ||
+      (a.h_out && a.h_stride < a.dim) || (a.q_out && a.q_stride < a.dim) ||
+      (a.gate && a.gate_stride != 0 && a.gate_stride < a.dim) ||
+      (a.q_out && a.q_scales_stride < (a.dim + kBlk - 1) / kBlk))
+    return EFFORT_ERR_ARG;
+  if (a.rows > EFFORT_MAX_ROWS || a.dim > EFFORT_MAX_IN_DIM) return EFFORT_ERR_UNSUPPORTED;
+  if (a.rows == 0) return EFFORT_OK;
+  int sms = 0;
+  effort_status_t st = device_sms(&sms);
+  if (st != EFFORT_OK) return st;
+  return launched(launch_block_norm(a, sms, (cudaStream_t)stream));
+}
+
+effort_status_t effort_fp8_prepare(const void* q, const float* scales, int64_t in_dim, int64_t out_dim, void* stream,
+                                   effort_fp8_t* out_matrix) {
+  if (!out_matrix) return EFFORT_ERR_ARG;
+  *out_matrix = nullptr;
+  if (!q || !scales || !aligned(scales, 4) || in_dim < 1 || out_dim < 1) return EFFORT_ERR_ARG;
+  if (in_dim > EFFORT_MAX_FP8_DIM || out_dim > EFFORT_MAX_FP8_DIM || in_dim * out_dim >= (1ll << 36))
+    return EFFORT_ERR_UNSUPPORTED;
+  const int nkb = cdiv(in_dim, kBlk), nsb = cdiv(out_dim, kBlk), cores = nsb * 16;
+  const size_t wbytes = (size_t)cores * nkb * kCoreBytes, sbytes = align_up((size_t)nkb * nsb * 4, 256);
+  if (!within_cap(wbytes + sbytes + 256)) return EFFORT_ERR_NOMEM;
+  effort_fp8_s* m = new (std::nothrow) effort_fp8_s();
+  if (!m) return EFFORT_ERR_NOMEM;
+  auto fail = [&](effort_status_t s) {
+    cudaGetLastError();
+    m->buf.release();
+    delete m;
+    return s;
+  };
+  if (cudaGetDevice(&m->dev) != cudaSuccess) return fail(EFFORT_ERR_CUDA);
+  effort_status_t st = m->buf.alloc(wbytes + sbytes + 256);
+  if (st != EFFORT_OK) return fail(st);
+  m->I = in_dim;
+  m->O = out_dim;
+  m->w = {(const uint8_t*)m->buf.p, cores, nkb, wbytes};
+  m->ws = (const float*)((char*)m->buf.p + wbytes);
+  unsigned* status = (unsigned*)((char*)m->buf.p + wbytes + sbytes);
+  cudaStream_t s = (cudaStream_t)stream;
+  unsigned bad = 0;
+  cudaError_t e = cudaMemsetAsync(status, 0, 4, s);
+  if (e == cudaSuccess)
+    e = launch_tile_weights(kWE4M3, q, 1, (int)in_dim, (int)out_dim, (uint8_t*)m->buf.p, cores, nkb, wbytes, 0, status, s);
+  if (e == cudaSuccess) e = launch_check_finite(scales, (size_t)nkb * nsb, status, s);
+  if (e == cudaSuccess) e = cudaMemcpyAsync((void*)m->ws, scales, (size_t)nkb * nsb * 4, cudaMemcpyDeviceToDevice, s);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&bad, status, 4, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return fail(EFFORT_ERR_CUDA);
+  if (bad) return fail(EFFORT_ERR_NONFINITE);
+  *out_matrix = m;
+  return EFFORT_OK;
+}
+
+effort_status_t effort_fp8_matmul(effort_fp8_t m, const void* x, int64_t x_stride, const float* x_scales,
+                                  int64_t x_scales_stride, int64_t rows, effort_dtype_t out_dtype, void* out,
+                                  int64_t out_stride, void* stream) {
+  if (!m || rows < 0 || !dtype_ok(out_dtype)) return EFFORT_ERR_ARG;
+  if (rows > 0 && (!x || !x_scales || !out)) return EFFORT_ERR_ARG;
+  if (!aligned(x, 16) || x_stride % 16 != 0 || x_stride < m->I || !aligned(x_scales, 4) || x_scales_stride < m->w.nkb)
+    return EFFORT_ERR_ARG;
+  if (!aligned(out, dtype_size(out_dtype)) || out_stride < m->O) return EFFORT_ERR_ARG;
+  if (rows > EFFORT_MAX_ROWS) return EFFORT_ERR_UNSUPPORTED;
+  if (rows == 0) return EFFORT_OK;
+  DeviceGuard guard(m->dev);
+  return launched(launch_fp8_matmul(m->w, m->ws, (int)m->I, (int)m->O, (const uint8_t*)x, x_stride, x_scales,
+                                    x_scales_stride, rows, out_dtype, out, out_stride, (cudaStream_t)stream));
+}
+
+effort_status_t effort_fp8_get_info(effort_fp8_t m, int64_t* in_dim, int64_t* out_dim, size_t* device_bytes) {
+  if (!m) return EFFORT_ERR_ARG;
+  if (in_dim) *in_dim = m->I;
+  if (out_dim) *out_dim = m->O;
+  if (device_bytes) *device_bytes = m->buf.bytes;
+  return EFFORT_OK;
+}
+
+effort_status_t effort_fp8_destroy(effort_fp8_t m) {
+  if (!m) return EFFORT_ERR_ARG;
+  {
+    DeviceGuard guard(m->dev);
+    m->buf.release();
+  }
+  delete m;
+  return EFFORT_OK;
+}
+
+effort_status_t effort_moe_prepare(const effort_moe_weights_t* weights, void* stream, effort_moe_t* out_layer) {
+  if (!out_layer) return EFFORT_ERR_ARG;
+  *out_layer = nullptr;
+  if (!weights) return EFFORT_ERR_ARG;
+  const effort_moe_weights_t& a = *weights;
+  const bool q = a.weight_kind == EFFORT_W_E4M3;
+  if (a.n_experts < 1 || a.in_dim < 1 || a.hidden_dim < 1 || !a.w1 || !a.w3 || !a.w2) return EFFORT_ERR_ARG;
+  if (!q && a.weight_kind != EFFORT_W_F16 && a.weight_kind != EFFORT_W_BF16) return EFFORT_ERR_ARG;
+  if (q ? (!a.s1 || !a.s3 || !a.s2) : (a.s1 || a.s3 || a.s2)) return EFFORT_ERR_ARG;
+  const size_t esz = q ? 1 : 2;
+  if (!aligned(a.w1, esz) || !aligned(a.w3, esz) || !aligned(a.w2, esz) || !aligned(a.s1, 4) || !aligned(a.s3, 4) ||
+      !aligned(a.s2, 4))
+    return EFFORT_ERR_ARG;
+  if (a.router && (!dtype_ok(a.router_dtype) || !aligned(a.router, dtype_size(a.router_dtype)))) return EFFORT_ERR_ARG;
+  if (a.n_experts > EFFORT_MAX_EXPERTS || a.in_dim > EFFORT_MAX_IN_DIM || a.hidden_dim > EFFORT_MAX_IN_DIM)
+    return EFFORT_ERR_UNSUPPORTED;
+  const int E = a.n_experts, I = (int)a.in_dim, F = (int)a.hidden_dim, wk = (int)a.weight_kind;
+  const int ke = k_per_block(wk);
+  const TileMat w13 = {nullptr, 2 * cdiv(F, 8), cdiv(I, ke), (size_t)2 * cdiv(F, 8) * cdiv(I, ke) * kCoreBytes};
+  const TileMat w2 = {nullptr, cdiv(I, 8), cdiv(F, ke), (size_t)cdiv(I, 8) * cdiv(F, ke) * kCoreBytes};
+  const size_t scale_n = (size_t)E * cdiv(I, kBlk) * cdiv(F, kBlk);
+  const size_t sbytes = q ? align_up(scale_n * 4, 256) : 0;
+  const size_t rbytes = a.router ? align_up((size_t)E * I * dtype_size(a.router_dtype), 256) : 0;
+  const size_t total = E * (w13.stride + w2.stride) + 3 * sbytes + rbytes + 256;
+  if (!within_cap(total)) return EFFORT_ERR_NOMEM;
+  effort_moe_s* h = new (std::nothrow) effort_moe_s();
+  if (!h) return EFFORT_ERR_NOMEM;
+  auto fail = [&](effort_status_t s) {
+    cudaGetLastError();
+    h->buf.release();
+    delete h;
+    return s;
+  };
+  if (cudaGetDevice(&h->dev) != cudaSuccess) return fail(EFFORT_ERR_CUDA);
+  effort_status_t st = h->buf.alloc(total);
+  if (st != EFFORT_OK) return fail(st);
+  h->E = E;
+  h->I = I;
+  h->F = F;
+  h->wk = wk;
+  h->rdt = (int)a.router_dtype;
+  char* b = (char*)h->buf.p;
+  h->w13 = w13;
+  h->w13.data = (const uint8_t*)b;
+  b += E * w13.stride;
+  h->w2 = w2;
+  h->w2.data = (const uint8_t*)b;
+  b += E * w2.stride;
+  const float** dst[3] = {&h->s1, &h->s3, &h->s2};
+  const float* src[3] = {a.s1, a.s3, a.s2};
+  unsigned* status = (unsigned*)((char*)h->buf.p + total - 256);
+  cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e = cudaMemsetAsync(status, 0, 4, s);
+  for (int i = 0; i < 3 && q; ++i) {
+    *dst[i] = (const float*)b;
+    if (e == cudaSuccess) e = launch_check_finite(src[i], scale_n, status, s);
+    if (e == cudaSuccess) e = cudaMemcpyAsync(b, src[i], scale_n * 4, cudaMemcpyDeviceToDevice, s);
+    b += sbytes;
+  }
+  if (a.router) {
+    h->router = b;
+    if (e == cudaSuccess)
+      e = cudaMemcpyAsync(b, a.router, (size_t)E * I * dtype_size(a.router_dtype), cudaMemcpyDeviceToDevice, s);
+  }
+  if (e == cudaSuccess)
+    e = launch_tile_weights(wk, a.w1, E, I, F, (uint8_t*)h->w13.data, w13.cores, w13.nkb, w13.stride, 1, status, s);
+  if (e == cudaSuccess)
+    e = launch_tile_weights(wk, a.w3, E, I, F, (uint8_t*)h->w13.data, w13.cores, w13.nkb, w13.stride, 2, status, s);
+  if (e == cudaSuccess)
+    e = launch_tile_weights(wk, a.w2, E, F, I, (uint8_t*)h->w2.data, w2.cores, w2.nkb, w2.stride, 0, status, s);
+  unsigned bad = 0;
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&bad, status, 4, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return fail(EFFORT_ERR_CUDA);
+  if (bad) return fail(EFFORT_ERR_NONFINITE);
+  *out_layer = h;
+  return EFFORT_OK;
+}
+
+effort_status_t effort_moe_scratch_bytes(effort_moe_t h, int64_t n_tokens, int32_t top_k, size_t* bytes) {
+  if (!h || !bytes || n_tokens < 0 || top_k < 1) return EFFORT_ERR_ARG;
+  if (n_tokens > EFFORT_MAX_TOKENS || top_k > EFFORT_MAX_TOP_K) return EFFORT_ERR_UNSUPPORTED;
+  *bytes = moe_scratch_bytes((int)n_tokens, top_k, (int)h->F, h->wk);
+  return EFFORT_OK;
+}
+
+effort_status_t effort_moe_forward(effort_moe_t h, const void* x, effort_dtype_t x_dtype, int64_t x_stride,
+                                   int64_t n_tokens, int32_t top_k, effort_gate_mode_t gate_mode, int32_t* ids,
+                                   float* gates, void* out, effort_dtype_t out_dtype, int64_t out_stride, void* scratch,
+                                   size_t scratch_bytes, void* stream) {
+  if (!h || n_tokens < 0 || top_k < 1 || !dtype_ok(x_dtype) || !dtype_ok(out_dtype)) return EFFORT_ERR_ARG;
+  if (gate_mode != EFFORT_GATE_SOFTMAX_OF_TOP && gate_mode != EFFORT_GATE_TOP_OF_SOFTMAX && gate_mode != EFFORT_GATE_GIVEN)
+    return EFFORT_ERR_ARG;
+  if (gate_mode != EFFORT_GATE_GIVEN && (!h->router || top_k > h->E)) return EFFORT_ERR_ARG;
+  if (n_tokens > 0 && (!x || !ids || !gates || !out || !scratch)) return EFFORT_ERR_ARG;
+  if (!aligned(x, dtype_size(x_dtype)) || !aligned(out, dtype_size(out_dtype)) || !aligned(ids, 4) || !aligned(gates, 4) ||
+      !aligned(scratch, 256) || x_stride < h->I || out_stride < h->I)
+    return EFFORT_ERR_ARG;
+  if (n_tokens > EFFORT_MAX_TOKENS || top_k > EFFORT_MAX_TOP_K) return EFFORT_ERR_UNSUPPORTED;
+  if (n_tokens == 0) return EFFORT_OK;
+  if (scratch_bytes < moe_scratch_bytes((int)n_tokens, top_k, (int)h->F, h->wk)) return EFFORT_ERR_ARG;
+  DeviceGuard guard(h->dev);
+  MoeCall c = {};
+  c.w13 = h->w13;
+  c.w2 = h->w2;
+  c.s1 = h->s1;
+  c.s3 = h->s3;
+  c.s2 = h->s2;
+  c.nsb13 = cdiv(h->F, kBlk);
+  c.nsb2 = cdiv(h->I, kBlk);
+  c.router = h->router;
+  c.rdt = h->rdt;
+  c.wk = h->wk;
+  c.n_experts = h->E;
+  c.I = (int)h->I;
+  c.F = (int)h->F;
+  c.x = x;
+  c.xdt = x_dtype;
+  c.xstride = x_stride;
+  c.n_tokens = (int)n_tokens;
+  c.top_k = top_k;
+  c.gate_mode = gate_mode;
+  c.ids = ids;
+  c.gates = gates;
+  c.out = out;
+  c.odt = out_dtype;
+  c.ostride = out_stride;
+  c.h = (float*)scratch;
+  c.hstride = (int64_t)h->w2.nkb * k_per_block(h->wk);
+  return launched(launch_moe(c, (cudaStream_t)stream));
+}
+
+effort_status_t effort_moe_get_info(effort_moe_t h, int32_t* n_experts, int64_t* in_dim, int64_t* hidden_dim,
+                                    size_t* device_bytes) {
+  if (!h) return EFFORT_ERR_ARG;
+  if (n_experts) *n_experts = h->E;
+  if (in_dim) *in_dim = h->I;
+  if (hidden_dim) *hidden_dim = h->F;
+  if (device_bytes) *device_bytes = h->buf.bytes;
+  return EFFORT_OK;
+}
+
+effort_status_t effort_moe_destroy(effort_moe_t h) {
+  if (!h) return EFFORT_ERR_ARG;
+  {
+    DeviceGuard guard(h->dev);
+    h->buf.release();
+  }
+  delete h;
+  return EFFORT_OK;
+}
+
+}  // extern "C"

@@ -50,7 +50,9 @@ typedef enum {
   EFFORT_ERR_UNSUPPORTED = 6   /* sizes outside the limits stated below */
 } effort_status_t;
 
-typedef enum { EFFORT_F32 = 0, EFFORT_F16 = 1 } effort_dtype_t;
+/* EFFORT_BF16 is taken by the feed-forward operators below; the Effort matvec
+ * entry points take EFFORT_F32 and EFFORT_F16 and refuse it. */
+typedef enum { EFFORT_F32 = 0, EFFORT_F16 = 1, EFFORT_BF16 = 2 } effort_dtype_t;
 
 /* Size limits of this build. */
 #define EFFORT_MAX_OUT_DIM 32768      /* a row is sorted inside one thread block */
@@ -357,6 +359,191 @@ effort_status_t effort_workspace_last_call_bytes(effort_workspace_t ws, uint64_t
  * workspaces of the process (the figure EFFORT_ALLOC_CAP_BYTES is checked
  * against).  bytes: host pointer, non-NULL. */
 effort_status_t effort_device_bytes_held(uint64_t* bytes);
+
+/* ------------------------------------------------------------------------
+ * Operators of the feed-forward block around the matvecs: the step between
+ * two blocks (norms, gate, residual, quantisation), the product with e4m3
+ * operands, and the mixture-of-experts layer for a few tokens.  The pages have
+ * no counterpart; they name the norm-joined matvec chain and the mixture of
+ * experts that these serve.  They are exact operators: no effort, no cutoff.
+ *
+ * They hold to the conventions above (device pointers owned by the caller,
+ * stream as void*, argument errors found on the host before any launch), and
+ * beyond them:
+ *  - Strides are in elements, between rows; elements of a row are adjacent.
+ *  - Sums, statistics and scales are held in fp32; each output is rounded once.
+ *  - No call allocates, synchronises or keeps anything between calls: any of
+ *    them may run on several streams at once, on one handle too, and may be
+ *    captured into a graph.
+ *  - rows (n_tokens) may be 0: nothing is launched.  Rows of an output beyond
+ *    the call's rows, and elements between dim and the stride, are not touched.
+ *  - inf and NaN follow IEEE arithmetic within their own row (token) and reach
+ *    no other row.
+ * ---------------------------------------------------------------------- */
+#define EFFORT_BLOCK 128        /* elements that share one scale of an e4m3 operand */
+#define EFFORT_MAX_FP8_DIM 262144   /* in_dim and out_dim of an e4m3 matrix */
+#define EFFORT_MAX_ROWS (1 << 24)   /* rows of one call */
+
+typedef enum { EFFORT_NORM_NONE = 0, EFFORT_NORM_RMS = 1, EFFORT_NORM_LAYER = 2 } effort_norm_kind_t;
+
+/*
+ * effort_block_norm -- the step between one block of a decoder layer and the
+ * next, row by row, in one kernel:
+ *
+ *   u  = post(y)                                      (post_kind; NONE: y)
+ *   x' = residual_scale * x + branch_scale * gate * u (y NULL: residual_scale * x)
+ *   h  = pre(x')                                      (pre_kind; NONE: x')
+ *
+ *   RMS:   n(v) = v / sqrt(mean(v^2) + eps) * (weight_offset + weight) + bias
+ *   LAYER: n(v) = (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) * (weight_offset + weight) + bias
+ *
+ * (a null weight multiplies by 1, whatever weight_offset is; a null bias adds
+ * nothing).  Outputs, each nullable, one at least given:
+ *   x_out  x' rounded to dtype.
+ *   h_out  h rounded to h_dtype.
+ *   q_out, q_scales  h in e4m3 with a scale per row and EFFORT_BLOCK columns:
+ *     scale = max |h| over the block / 448 (fp32), q = h / scale rounded to
+ *     nearest even; a block of zeros (or one whose scale underflows to zero)
+ *     has scale 0 and q 0.  A block that holds inf or NaN has scale inf or NaN.
+ *     This is the form effort_fp8_matmul takes.
+ * h is computed from x' before x' is rounded.
+ *   dtype: of x, y, gate and x_out.  weight_dtype: of all weights and biases [dim].
+ *   gate: nullable; gate_stride 0 uses one row for all rows.
+ *   1 <= dim <= EFFORT_MAX_IN_DIM, 0 <= rows <= EFFORT_MAX_ROWS; every stride
+ *   (but gate's 0) is at least dim (q_scales_stride: at least its blocks).
+ *   Pointers are aligned to their element type.
+ *   x_out and h_out may be the same array as x or y (same address, element
+ *   size and stride); they overlap nothing else, nor one another.
+ *   Runs on the current device, where all pointers have to live.
+ */
+typedef struct {
+  int64_t rows, dim;
+  effort_dtype_t dtype, weight_dtype, h_dtype;
+  effort_norm_kind_t post_kind, pre_kind;
+  float eps, weight_offset, residual_scale, branch_scale;
+  const void* x;
+  int64_t x_stride;
+  const void* y;
+  int64_t y_stride;
+  const void* gate;
+  int64_t gate_stride;
+  const void *post_weight, *post_bias, *pre_weight, *pre_bias;
+  void* x_out;
+  int64_t x_out_stride;
+  void* h_out;
+  int64_t h_stride;
+  void* q_out;
+  int64_t q_stride;
+  float* q_scales;
+  int64_t q_scales_stride;
+} effort_block_norm_t;
+
+effort_status_t effort_block_norm(const effort_block_norm_t* args, void* stream);
+
+/*
+ * effort_fp8_prepare -- an e4m3 weight matrix with one fp32 scale per 128 x 128
+ *   block, laid out for effort_fp8_matmul: w_ij = scales[i / 128][j / 128] * q_ij.
+ *   q: device e4m3 bytes [in_dim x out_dim], row-major (row i multiplies
+ *   x[i]); scales: device fp32 [ceil(in_dim / 128) x ceil(out_dim / 128)],
+ *   4-byte aligned.  Both are read during the call only (the stream is
+ *   synchronised before returning).
+ *   1 <= in_dim, out_dim <= EFFORT_MAX_FP8_DIM, in_dim * out_dim < 2^36.
+ *   Returns EFFORT_ERR_NONFINITE if q holds a NaN or a scale is inf or NaN,
+ *   EFFORT_ERR_NOMEM as effort_prepare does.
+ *   The handle holds one byte per weight (both dims rounded up to 128) and the scales.
+ */
+typedef struct effort_fp8_s* effort_fp8_t;
+effort_status_t effort_fp8_prepare(const void* q, const float* scales, int64_t in_dim, int64_t out_dim, void* stream,
+                                   effort_fp8_t* out_matrix);
+
+/*
+ * effort_fp8_matmul -- out[r][n] = sum over blocks b of 128 of
+ *     x_scales[r][b] * scales[b][n / 128] * sum over k in b of x[r][k] q[k][n].
+ *   x: device e4m3 bytes [rows x in_dim], 16-byte aligned, x_stride a multiple
+ *   of 16 (what effort_block_norm writes for such a q_out); x_scales: device
+ *   fp32 [rows x ceil(in_dim / 128)].  out: [rows x out_dim] of out_dtype.
+ *   0 <= rows <= EFFORT_MAX_ROWS.  out overlaps neither input.
+ *   One kernel; results do not vary from call to call.
+ */
+effort_status_t effort_fp8_matmul(effort_fp8_t m, const void* x, int64_t x_stride, const float* x_scales,
+                                  int64_t x_scales_stride, int64_t rows, effort_dtype_t out_dtype, void* out,
+                                  int64_t out_stride, void* stream);
+
+effort_status_t effort_fp8_get_info(effort_fp8_t m, int64_t* in_dim, int64_t* out_dim, size_t* device_bytes);
+
+/* Frees the matrix's device storage.  The caller has synchronised the streams
+ * that use it. */
+effort_status_t effort_fp8_destroy(effort_fp8_t m);
+
+/*
+ * effort_moe_prepare -- the weights of a mixture-of-experts layer, laid out
+ *   for effort_moe_forward.  Expert e computes
+ *     y = W2_e^T (silu(W1_e^T x) * (W3_e^T x)),  silu(a) = a / (1 + exp(-a)).
+ *   w1, w3: device [n_experts x in_dim x hidden_dim], w2: device [n_experts x
+ *   hidden_dim x in_dim], row-major, aligned to their element; weight_kind
+ *   gives their type.  EFFORT_W_E4M3: e4m3 bytes with s1, s3 [n_experts x
+ *   ceil(in_dim / 128) x ceil(hidden_dim / 128)] and s2 [n_experts x
+ *   ceil(hidden_dim / 128) x ceil(in_dim / 128)] fp32; else s1, s3, s2 are NULL.
+ *   router: device [n_experts x in_dim] of router_dtype, row-major; nullable
+ *   (every call then brings its routing).
+ *   All are read during the call only (the stream is synchronised before
+ *   returning); the handle keeps its own copies.
+ *   1 <= n_experts <= EFFORT_MAX_EXPERTS, 1 <= in_dim, hidden_dim <= EFFORT_MAX_IN_DIM.
+ *   Returns EFFORT_ERR_NONFINITE if a weight or scale is inf or NaN.
+ */
+#define EFFORT_MAX_EXPERTS 256
+#define EFFORT_MAX_TOKENS 256   /* n_tokens of one call */
+#define EFFORT_MAX_TOP_K 16
+typedef enum { EFFORT_W_F16 = 0, EFFORT_W_BF16 = 1, EFFORT_W_E4M3 = 2 } effort_weight_kind_t;
+typedef struct effort_moe_s* effort_moe_t;
+typedef struct {
+  int32_t n_experts;
+  int64_t in_dim, hidden_dim;
+  effort_weight_kind_t weight_kind;
+  const void *w1, *w3, *w2;
+  const float *s1, *s3, *s2;
+  const void* router;
+  effort_dtype_t router_dtype;
+} effort_moe_weights_t;
+effort_status_t effort_moe_prepare(const effort_moe_weights_t* weights, void* stream, effort_moe_t* out_layer);
+
+/*
+ * effort_moe_forward -- the layer on a few tokens:
+ *     out[t] = sum over j < top_k of gates[t][j] * expert_{ids[t][j]}(x[t]).
+ *   gate_mode
+ *     EFFORT_GATE_SOFTMAX_OF_TOP: logits l = router x[t]; ids = the top_k
+ *       largest, in falling order, ties to the lower expert; gates = softmax
+ *       over the chosen logits.  ids and gates are written.
+ *     EFFORT_GATE_TOP_OF_SOFTMAX: the same ids; gates = the chosen entries of
+ *       the softmax over all experts (not renormalised).
+ *     EFFORT_GATE_GIVEN: ids and gates are read.  An id below 0 or at or above
+ *       n_experts adds nothing (padding); a token may name one expert twice.
+ *   x: device [n_tokens x in_dim] of x_dtype; out: device [n_tokens x in_dim] of
+ *   out_dtype, fully written (0 where every id is out of range); ids: device
+ *   int32 [n_tokens x top_k], gates: device fp32 [n_tokens x top_k], packed.
+ *   0 <= n_tokens <= EFFORT_MAX_TOKENS, 1 <= top_k <= EFFORT_MAX_TOP_K, and top_k <=
+ *   n_experts unless the routing is given.
+ *   scratch: device memory of effort_moe_scratch_bytes(layer, n_tokens, top_k)
+ *   bytes, 256-byte aligned, whose contents mean nothing before and after the
+ *   call; calls that may overlap on the GPU bring scratch of their own.
+ *   A token whose logits hold NaN counts them as lowest; its gates are NaN.
+ */
+typedef enum {
+  EFFORT_GATE_SOFTMAX_OF_TOP = 0,
+  EFFORT_GATE_TOP_OF_SOFTMAX = 1,
+  EFFORT_GATE_GIVEN = 2
+} effort_gate_mode_t;
+effort_status_t effort_moe_scratch_bytes(effort_moe_t layer, int64_t n_tokens, int32_t top_k, size_t* bytes);
+effort_status_t effort_moe_forward(effort_moe_t layer, const void* x, effort_dtype_t x_dtype, int64_t x_stride,
+                                   int64_t n_tokens, int32_t top_k, effort_gate_mode_t gate_mode, int32_t* ids,
+                                   float* gates, void* out, effort_dtype_t out_dtype, int64_t out_stride, void* scratch,
+                                   size_t scratch_bytes, void* stream);
+effort_status_t effort_moe_get_info(effort_moe_t layer, int32_t* n_experts, int64_t* in_dim, int64_t* hidden_dim,
+                                    size_t* device_bytes);
+
+/* Frees the layer's device storage.  The caller has synchronised the streams
+ * that use it. */
+effort_status_t effort_moe_destroy(effort_moe_t layer);
 
 /* Static string naming a status code. */
 const char* effort_status_string(effort_status_t s);
