@@ -22,6 +22,7 @@ namespace effort {
 constexpr int kBlk = 128;            // elements that share one scale
 constexpr int kCoreBytes = 1024;     // 8 rows x 128 bytes
 constexpr float kE4M3Max = 448.0f;
+constexpr int kMaxDevices = 64;      // devices whose launch limits are remembered
 
 // element types of activations and outputs (effort_dtype_t)
 enum : int { kF32 = 0, kF16 = 1, kBF16 = 2 };
