@@ -14,6 +14,7 @@ cudaError_t launch_block_norm(const effort_block_norm_t& a, int sms, cudaStream_
 cudaError_t launch_tile_weights(int wk, const void* w, int mats, int K, int N, uint8_t* out, int cores, int nkb,
                                 size_t stride, int pair, unsigned* status, cudaStream_t s);
 cudaError_t launch_check_finite(const float* p, size_t n, unsigned* status, cudaStream_t s);
+cudaError_t launch_turn_scales(const float* s, int mats, int nkb, int nsb, float* out, cudaStream_t st);
 cudaError_t launch_fp8_matmul(const TileMat& w, const float* ws, int I, int O, const uint8_t* x, int64_t xstride,
                               const float* xs, int64_t xsstride, int64_t rows, int odt, void* out, int64_t ostride,
                               cudaStream_t s);
@@ -108,7 +109,7 @@ effort_status_t effort_fp8_prepare(const void* q, const float* scales, int64_t i
   if (in_dim > EFFORT_MAX_FP8_DIM || out_dim > EFFORT_MAX_FP8_DIM || in_dim * out_dim >= (1ll << 36))
     return EFFORT_ERR_UNSUPPORTED;
   const int nkb = cdiv(in_dim, kBlk), nsb = cdiv(out_dim, kBlk), cores = nsb * 16;
-  const size_t wbytes = (size_t)cores * nkb * kCoreBytes, sbytes = align_up((size_t)nkb * nsb * 4, 256);
+  const size_t wbytes = (size_t)cores * nkb * kCoreBytes, sbytes = align_up((size_t)align4(nkb) * nsb * 4, 256);
   if (!within_cap(wbytes + sbytes + 256)) return EFFORT_ERR_NOMEM;
   effort_fp8_s* m = new (std::nothrow) effort_fp8_s();
   if (!m) return EFFORT_ERR_NOMEM;
@@ -132,7 +133,7 @@ effort_status_t effort_fp8_prepare(const void* q, const float* scales, int64_t i
   if (e == cudaSuccess)
     e = launch_tile_weights(kWE4M3, q, 1, (int)in_dim, (int)out_dim, (uint8_t*)m->buf.p, cores, nkb, wbytes, 0, status, s);
   if (e == cudaSuccess) e = launch_check_finite(scales, (size_t)nkb * nsb, status, s);
-  if (e == cudaSuccess) e = cudaMemcpyAsync((void*)m->ws, scales, (size_t)nkb * nsb * 4, cudaMemcpyDeviceToDevice, s);
+  if (e == cudaSuccess) e = launch_turn_scales(scales, 1, nkb, nsb, (float*)m->ws, s);
   if (e == cudaSuccess) e = cudaMemcpyAsync(&bad, status, 4, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return fail(EFFORT_ERR_CUDA);

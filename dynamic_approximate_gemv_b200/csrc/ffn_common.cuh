@@ -32,6 +32,8 @@ enum : int { kWF16 = 0, kWBF16 = 1, kWE4M3 = 2 };
 __host__ __device__ inline int k_per_block(int wk) { return wk == kWE4M3 ? 128 : 64; }
 __host__ __device__ inline int cdiv(long long a, long long b) { return (int)((a + b - 1) / b); }
 
+__host__ __device__ inline int align4(int x) { return (x + 3) & ~3; }
+
 // byte offset of element k (of esz bytes) of row r inside a core
 __device__ __forceinline__ int core_offset(int r, int k, int esz) {
   const int b = k * esz;

@@ -86,8 +86,8 @@ cudaError_t launch_check_finite(const float* p, size_t n, unsigned* status, cuda
 // shared memory, so there is no scratch and no order that varies.
 struct FewRows {
   TileMat w;
-  const float* ws;
-  int nsb, I, O, rows;
+  const float* ws;   // [row block][K block], rows of nkb4 floats
+  int nkb4, I, O, rows;
   const uint8_t* x;
   long long xstride;
   const float* xs;
@@ -96,55 +96,76 @@ struct FewRows {
   long long ostride;
   int odt, tiles, cluster, kw;
 };
+constexpr int kFewRowsMax = 16;
 
 template <int NT>
-struct FewRowsCfg {
-  static constexpr int kMT = NT == 4 ? 2 : 4;      // tiles of a group
-  static constexpr int kStages = NT == 4 ? 5 : 3;  // 20 or 24 KB of ring for each warp
-  static constexpr int kStageBytes = kMT * 2 * kCoreBytes;
-  static constexpr int kPitch = kMT * 16 + 4;      // floats of one column in the join; + 4: no bank met twice
-  static constexpr int kRed = NT * 8 * kPitch;     // floats of one warp's part
-  static constexpr size_t kBars = 0, kRing = 1024, kRedAt = kRing + (size_t)kSWarps * kStages * kStageBytes;
-  static constexpr size_t kSmem = kRedAt + (size_t)kSWarps * kRed * 4;
-  static_assert(kSmem <= 227 * 1024, "one block per SM");
-};
-
-template <int NT>
-__global__ void __launch_bounds__(kSThreads, 1) k_fp8_few_rows(const FewRows a) {
-  using C = FewRowsCfg<NT>;
-  constexpr int MT = C::kMT;
+__global__ void __launch_bounds__(StreamShape<NT, 128>::kThreads, 1) k_fp8_few_rows(const FewRows a) {
+  using S = StreamShape<NT, 128>;
+  constexpr int MT = S::kMT;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
-  float* red = reinterpret_cast<float*>(smem + C::kRedAt);
+  float* red = reinterpret_cast<float*>(smem + S::kRedAt);
+  const uint32_t xtab = sbase + S::kExtraAt;  // x_scales of the block's K blocks: [K block][NT * 8]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
   const int cl = a.cluster, rank = cl > 1 ? (int)cluster_rank() : 0;
   const int ncl = gridDim.x / cl, c = blockIdx.x / cl;
   const int t0 = (int)((long long)a.tiles * c / ncl), t1 = (int)((long long)a.tiles * (c + 1) / ncl);
   const int kb0 = a.w.nkb * rank / cl, kb1 = a.w.nkb * (rank + 1) / cl;
-  const int kw = a.kw, rw = kSWarps / kw, wk = warp % kw, wr = warp / kw;
+  const int kw = a.kw, rw = S::kWarps / kw, wk = warp % kw, wr = warp / kw;
   const int groups = cdiv(t1 - t0, MT);
-  const size_t core_stride = (size_t)a.w.nkb * kCoreBytes;
 
-  Ring<C::kStages, C::kStageBytes> ring;
-  ring.init(sbase + C::kRing, sbase + C::kBars, warp, lane);
-  // the warp's list: groups wr, wr + rw, ..; in each the K blocks kb0 + wk, + kw, ..
+  Ring<S> ring;
+  ring.init(sbase, warp, lane);
+  // A stage: the cores and the scales (they do not depend on the kernel
+  // before), then the rows of x.  The warp's list: groups wr, wr + rw, ..; in
+  // each the K blocks kb0 + wk, + kw, ..
+  auto ask_weights = [&](int gi, int kb) {
+    const int t = t0 + gi * MT, n = min(MT, t1 - t);
+    const int last = a.I - kb * kBlk, xb = last >= kBlk ? kBlk : (last + 15) / 16 * 16;
+    const uint32_t buf = ring.next_buf(), bar = ring.next_bar();
+    const int two = (t + n - 1) / 8 > t / 8;  // the group's tiles lie in one or two blocks of 128 columns
+    if (lane == 0) mbar_expect(bar, n * 2 * kCoreBytes + a.rows * xb + 16 + 16 * two);
+    __syncwarp();
+    if (lane < 2 * n)
+      bulk_load(buf + lane * kCoreBytes, a.w.data + ((size_t)(2 * t + lane) * a.w.nkb + kb) * kCoreBytes, kCoreBytes, bar);
+    else if (lane >= 30 - two && lane < 31)
+      bulk_load(buf + S::kScaleAt + 16 * (30 - lane), a.ws + (size_t)(t / 8 + 30 - lane) * a.nkb4 + (kb & ~3), 16, bar);
+  };
+  auto ask_rows = [&](int kb) {
+    const int last = a.I - kb * kBlk, xb = last >= kBlk ? kBlk : (last + 15) / 16 * 16;
+    const uint32_t buf = ring.next_buf(), bar = ring.next_bar();
+    if (lane < a.rows) bulk_load(buf + S::kActAt + lane * S::kRowPitch, a.x + lane * a.xstride + kb * kBlk, xb, bar);
+    ++ring.put;
+  };
   int pg = wr, pk = kb0 + wk;
-  auto ask = [&]() {
-    if (pk >= kb1) return;  // no K block for this warp
-    if (pg >= groups) return;
-    const int t = t0 + pg * MT, n = min(MT, t1 - t);
-    ring.fill(a.w.data + ((size_t)(2 * t) * a.w.nkb + pk) * kCoreBytes, 2 * n, core_stride, lane);
+  const bool busy = pk < kb1;
+  auto step = [&]() {
     pk += kw;
     if (pk >= kb1) {
       pk = kb0 + wk;
       pg += rw;
     }
   };
-  // the weights do not depend on the kernel before
-#pragma unroll
-  for (int s = 0; s < C::kStages; ++s) ask();
+  // the first stages' weights ahead of the kernel before
+  int early = 0;
+  for (; early < S::kStages && busy && pg < groups; ++early) {
+    ask_weights(pg, pk);
+    ++ring.put;
+    step();
+  }
   grid_dep_launch();
   grid_dep_wait();
+  for (int i = threadIdx.x; i < (kb1 - kb0) * NT * 8; i += S::kThreads) {
+    const int r = i / (kb1 - kb0), k = i % (kb1 - kb0);
+    const float s = r < a.rows ? __ldg(a.xs + r * a.xsstride + kb0 + k) : 0.0f;
+    *reinterpret_cast<float*>(smem + S::kExtraAt + (k * NT * 8 + r) * 4) = s;
+  }
+  ring.put = 0;
+  for (int i = 0, k = kb0 + wk; i < early; ++i) {
+    ask_rows(k);
+    k = k + kw < kb1 ? k + kw : kb0 + wk;
+  }
+  __syncthreads();
 
   const int live = NT == 1 ? 1 : (a.rows + 7) / 8;
   bool fine = true;
@@ -158,61 +179,40 @@ __global__ void __launch_bounds__(kSThreads, 1) k_fp8_few_rows(const FewRows a) 
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.0f;
     for (int kb = kb0 + wk; kb < kb1; kb += kw) {
-      // B: column g of each tile is a row of x, elements 32 q .. 32 q + 31
-      uint32_t b[1][NT][8][2];
-      float sx[NT][2], sw[MT];
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        uint4 v[2] = {};
-        const int r = 8 * j + g;
-        if (r < a.rows) {
-          const uint8_t* p = a.x + r * a.xstride;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int k = kb * kBlk + 32 * q + 16 * h;
-            if (k < a.I) v[h] = __ldg(reinterpret_cast<const uint4*>(p + k));
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int rr = 8 * j + 2 * q + e;
-          sx[j][e] = rr < a.rows ? __ldg(a.xs + rr * a.xsstride + kb) : 0.0f;
-        }
-        if (kb == a.w.nkb - 1) {  // bytes behind the row's end count as zero
-          uint8_t* y = reinterpret_cast<uint8_t*>(v);
-          const int k = kb * kBlk + 32 * q;
-#pragma unroll
-          for (int h = 0; h < 32; ++h)
-            if (k + h >= a.I) y[h] = 0;
-        }
-        const uint32_t u[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-#pragma unroll
-        for (int s = 0; s < 8; ++s) {
-          b[0][j][s][0] = e4m3x2_to_half2(u[s]);
-          b[0][j][s][1] = e4m3x2_to_half2(u[s] >> 16);
-        }
-      }
-#pragma unroll
-      for (int m = 0; m < MT; ++m) sw[m] = __ldg(a.ws + (size_t)kb * a.nsb + min((t + m) / 8, a.nsb - 1));
       uint32_t at;
       fine &= ring.wait(&at);
+      uint32_t b[1][NT][8][2];
+      float sx[NT][2], sw[2];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        act_e4m3(at + S::kActAt + (8 * j + g) * S::kRowPitch, q, 8 * j + g < a.rows, a.I - kb * kBlk, b[0][j]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) sx[j][e] = lds_float(xtab + ((kb - kb0) * NT * 8 + 8 * j + 2 * q + e) * 4);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) sw[h] = lds_float(at + S::kScaleAt + 16 * h + 4 * (kb & 3));
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         if (m < n) {
           float d[NT][4] = {};
           mma_tile<kWE4M3, NT, 1, 8>(at + m * 2 * kCoreBytes, g, q, b, live, d);
+          const float s = (t + m) / 8 == t / 8 ? sw[0] : sw[1];
 #pragma unroll
           for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[m][j][e] = fmaf(d[j][e] * sx[j][e & 1], sw[m], acc[m][j][e]);
+            for (int e = 0; e < 4; ++e) acc[m][j][e] = fmaf(d[j][e] * sx[j][e & 1], s, acc[m][j][e]);
         }
       }
       __syncwarp();  // every lane has read the stage
-      ask();
+      if (busy && pg < groups) {
+        ask_weights(pg, pk);
+        ask_rows(pk);
+        step();
+      }
     }
     // join the warps' sums (and the cluster's)
-    named_sync(1 + wr, kw * 32);
-    float* mine = red + warp * C::kRed;
+    named_sync(wr, kw * 32);
+    float* mine = red + warp * S::kRed;
     const float poison = fine ? 0.0f : __int_as_float(0x7fffffff);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -220,31 +220,32 @@ __global__ void __launch_bounds__(kSThreads, 1) k_fp8_few_rows(const FewRows a) 
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          mine[(8 * j + 2 * q + (e & 1)) * C::kPitch + 16 * m + g + 8 * (e >> 1)] = acc[m][j][e] + poison;
-    named_sync(1 + wr, kw * 32);
+          mine[(8 * j + 2 * q + (e & 1)) * S::kPitch + 16 * m + g + 8 * (e >> 1)] = acc[m][j][e] + poison;
+    named_sync(wr, kw * 32);
     const int outs = n * 16 * a.rows;
-    float* first = red + wr * kw * C::kRed;
+    float* first = red + wr * kw * S::kRed;
     if (cl == 1) {
       for (int i = threadIdx.x - wr * kw * 32; i < outs; i += kw * 32) {
         const int r = i / (n * 16), o = i % (n * 16), col = t * 16 + o;
         float s = 0.0f;
-        for (int w = 0; w < kw; ++w) s += first[w * C::kRed + r * C::kPitch + o];
+        for (int w = 0; w < kw; ++w) s += first[w * S::kRed + r * S::kPitch + o];
         if (col < a.O) store_dt(a.out, a.odt, r * a.ostride + col, s);
       }
     } else {
-      // kw = 8, rw = 1: the block's sum into the first warp's part, then each
+      // one set of warps: the block's sum into the first warp's part, then each
       // block takes its share of the outputs
-      for (int i = threadIdx.x; i < outs; i += kSThreads) {
-        const int at = i / (n * 16) * C::kPitch + i % (n * 16);
+      for (int i = threadIdx.x; i < outs; i += S::kThreads) {
+        const int at = i / (n * 16) * S::kPitch + i % (n * 16);
         float s = 0.0f;
-        for (int w = 0; w < kSWarps; ++w) s += red[w * C::kRed + at];
+#pragma unroll
+        for (int w = 0; w < S::kWarps; ++w) s += red[w * S::kRed + at];
         red[at] = s;
       }
       cluster_sync();
       const int i0 = outs * rank / cl, i1 = outs * (rank + 1) / cl;
-      for (int i = i0 + threadIdx.x; i < i1; i += kSThreads) {
+      for (int i = i0 + threadIdx.x; i < i1; i += S::kThreads) {
         const int r = i / (n * 16), o = i % (n * 16), col = t * 16 + o;
-        const uint32_t at = sbase + (uint32_t)C::kRedAt + (uint32_t)(r * C::kPitch + o) * 4;
+        const uint32_t at = sbase + (uint32_t)S::kRedAt + (uint32_t)(r * S::kPitch + o) * 4;
         float s = 0.0f;
         for (int w = 0; w < cl; ++w) s += remote_float(at, w);
         if (col < a.O) store_dt(a.out, a.odt, r * a.ostride + col, s);
@@ -259,8 +260,8 @@ template <int NT>
 static int few_rows_clusters(int cluster) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)cluster);
-  cfg.blockDim = dim3(kSThreads);
-  cfg.dynamicSmemBytes = FewRowsCfg<NT>::kSmem;
+  cfg.blockDim = dim3(StreamShape<NT, 128>::kThreads);
+  cfg.dynamicSmemBytes = StreamShape<NT, 128>::kSmem;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned)cluster;
@@ -284,7 +285,7 @@ static cudaError_t launch_few_rows(FewRows a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if (dev >= kMaxDevices) return cudaErrorInvalidDevice;
   if (fit[dev][0].load() == 0) {
-    e = cudaFuncSetAttribute(k_fp8_few_rows<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FewRowsCfg<NT>::kSmem);
+    e = cudaFuncSetAttribute(k_fp8_few_rows<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)StreamShape<NT, 128>::kSmem);
     if (e != cudaSuccess) return e;
     for (int i = 3; i >= 0; --i) fit[dev][i].store(few_rows_clusters<NT>(1 << i));
     if (fit[dev][0].load() < 1) return cudaErrorLaunchOutOfResources;
@@ -296,20 +297,23 @@ static cudaError_t launch_few_rows(FewRows a, cudaStream_t s) {
   for (int i = 0; i < 4; ++i) {
     const int cl = 1 << i, n = min(fit[dev][i].load(), a.tiles);
     if (n < 1 || cl > a.w.nkb) break;
-    const long long cost = (long long)cdiv(a.tiles, n) * cdiv(a.w.nkb, cl);
+    if ((long long)cdiv(a.w.nkb, cl) * NT * 8 * 4 > StreamShape<NT, 128>::kExtra) continue;  // the table of x's scales
+    const long long per = cdiv(a.tiles, n);
+    const long long cost = per * cdiv(a.w.nkb, cl) + (cl > 1 ? 24 * cdiv(per, StreamShape<NT, 128>::kMT) : 0);
     if (ncl == 0 || cost * 102 < best * 100) {
       best = cost;
       a.cluster = cl;
       ncl = n;
     }
   }
-  a.kw = kSWarps;
+  if (ncl == 0) return cudaErrorInvalidConfiguration;
+  a.kw = StreamShape<NT, 128>::kWarps;
   if (a.cluster == 1)
     while (a.kw > a.w.nkb) a.kw /= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(ncl * a.cluster));
-  cfg.blockDim = dim3(kSThreads);
-  cfg.dynamicSmemBytes = FewRowsCfg<NT>::kSmem;
+  cfg.blockDim = dim3(StreamShape<NT, 128>::kThreads);
+  cfg.dynamicSmemBytes = StreamShape<NT, 128>::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -326,13 +330,29 @@ cudaError_t launch_fp8_matmul(const TileMat& w, const float* ws, int I, int O, c
                               const float* xs, int64_t xsstride, int64_t rows, int odt, void* out, int64_t ostride,
                               cudaStream_t s) {
   const size_t osz = odt == kF32 ? 4 : 2;
-  for (int64_t r = 0; r < rows; r += 32) {
-    FewRows a = {w, ws, cdiv(O, kBlk), I, O, (int)(rows - r < 32 ? rows - r : 32), x + r * xstride, xstride,
-                 xs + r * xsstride, xsstride, (char*)out + r * ostride * osz, ostride, odt, cdiv(O, 16), 1, kSWarps};
-    cudaError_t e = a.rows <= 8 ? launch_few_rows<1>(a, s) : a.rows <= 16 ? launch_few_rows<2>(a, s) : launch_few_rows<4>(a, s);
+  // 16 rows' scales of a very long K do not fit beside the ring: 8 rows then
+  const int most = w.nkb > 1536 ? 8 : kFewRowsMax;
+  for (int64_t r = 0; r < rows; r += most) {
+    FewRows a = {w, ws, align4(w.nkb), I, O, (int)(rows - r < most ? rows - r : most), x + r * xstride,
+                 xstride, xs + r * xsstride, xsstride, (char*)out + r * ostride * osz, ostride, odt, cdiv(O, 16), 1, 1};
+    cudaError_t e = a.rows <= 8 ? launch_few_rows<1>(a, s) : launch_few_rows<2>(a, s);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
+}
+
+// Scales [in block][out block] as the products take them: [matrix][out block][in
+// block], rows of align4(in blocks) floats, so that 16 bytes hold four K blocks.
+__global__ void k_turn_scales(const float* s, int nkb, int nsb, float* out) {
+  const size_t m = blockIdx.y;
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < nsb * align4(nkb); i += gridDim.x * blockDim.x) {
+    const int b = i / align4(nkb), k = i % align4(nkb);
+    out[m * nsb * align4(nkb) + i] = k < nkb ? s[(m * nkb + k) * nsb + b] : 0.0f;
+  }
+}
+cudaError_t launch_turn_scales(const float* s, int mats, int nkb, int nsb, float* out, cudaStream_t st) {
+  k_turn_scales<<<dim3(64, (unsigned)mats), 256, 0, st>>>(s, nkb, nsb, out);
+  return cudaGetLastError();
 }
 
 }  // namespace effort

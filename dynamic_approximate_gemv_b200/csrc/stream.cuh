@@ -1,0 +1,246 @@
+// Products with few columns: device code shared by the e4m3 product (fp8.cu)
+// and the mixture of experts (moe.cu).
+//
+// What bounds them is the one read of the weights, so the kernel is built
+// around that stream.  One block per SM.  A block works through groups of up
+// to MT 16-row tiles; inside a group warp w multiplies the K blocks w, w + kw,
+// ...  Each warp owns a ring of stages in shared memory that it fills itself
+// with bulk copies and runs ahead through its whole list, across the groups'
+// borders, so no warp waits for another except in the join at a group's end.
+//
+// A stage brings everything one K block of a group needs: the weights' cores
+// (1 KB each), that K block of the activations' rows, and its scales.  The
+// activations come from L2 and are small, but a load of them that is issued
+// beside the stream waits behind the 100 KB an SM has asked for (3 us and
+// more, measured as 13.5 against 11.1 us at 4096 x 14336); in the stage they
+// arrive with the weights they meet.
+//
+// The products run on the warp-wide matrix instruction m16n8k16 (16 weight
+// rows, 8 columns, fp32 sums): with so few columns every operand byte is used
+// once and the larger instructions would wait for HBM just the same.  e4m3
+// weights become binary16 in registers (exact).  K may be permuted freely as
+// long as both operands agree: lane q of a row's four takes 32 consecutive
+// bytes, which are two 16-byte reads that meet no bank twice.
+#pragma once
+#include "ffn_common.cuh"
+
+namespace effort {
+
+constexpr int kMaxWaits = 1 << 18;  // tries of a wait before it gives up
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Bounded: false once the phase did not come.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+  for (int i = 0; i < kMaxWaits; ++i)
+    if (mbar_try(bar, parity)) return true;
+  return false;
+}
+// both addresses and the size are multiples of 16 bytes
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ float remote_float(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float lds_float(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+  if constexpr (BF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// two fp32 values to a pair of the matrix instruction's type, low half first
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if constexpr (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+  if constexpr (BF16) return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+// four e4m3 values as two pairs of binary16
+__device__ __forceinline__ void e4m3x4_to_half2(uint32_t w, uint32_t& a, uint32_t& b) {
+  asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
+      : "=r"(a), "=r"(b)
+      : "r"(w));
+}
+
+// Power of two that brings a block's largest magnitude into [2^14, 2^15), the
+// top of binary16's range, and its inverse.  Blocks below 2^-97 are scaled as
+// if they reached it.
+__device__ __forceinline__ void pow2_scale(float amax, float* up, float* down) {
+  int e = (int)((__float_as_uint(amax) >> 23) & 0xff);  // biased exponent; inf and NaN: 255
+  e = e < 30 ? 30 : e;
+  *up = __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23);
+  *down = __uint_as_float((uint32_t)(e - 14) << 23);
+}
+
+// ---------------------------------------------------------------- shapes
+// What a stage holds and how many fit: W warps, MT tiles a group, ST stages a
+// warp.  ROWB: bytes of one K block of an activation row.
+constexpr int kSmemMax = 227 * 1024;
+constexpr int kStreamHead = 2048;    // barriers
+template <int NT, int ROWB>
+struct StreamShape {
+  static constexpr int kRowPitch = ROWB + 16;  // rows 16 bytes apart in the banks: no read meets one twice
+  static constexpr int kActBytes = NT * 8 * kRowPitch;
+  static constexpr int stage(int mt) { return mt * 2 * kCoreBytes + kActBytes + 64; }
+  static constexpr int pitch(int mt) { return mt * 16 + 4; }  // floats of a column in the join, likewise
+  static constexpr int red(int w, int mt) { return w * NT * 8 * pitch(mt) * 4; }
+  static constexpr int stages(int w, int mt, int extra) {
+    const int n = (kSmemMax - kStreamHead - extra - red(w, mt)) / (w * stage(mt));
+    return n > 6 ? 6 : n;
+  }
+  // sixteen warps where two stages each fit (a K block's share of latency
+  // hides better than with eight: 12.3 against 14.5 us at 14336 x 4096)
+  static constexpr int kExtra = 12 * 1024;  // lists and scales of the caller
+  static constexpr bool k16 = stages(16, 2, kExtra) >= 2;
+  static constexpr bool k84 = stages(8, 4, kExtra) >= 2;
+  static constexpr int kWarps = k16 ? 16 : 8;
+  static constexpr int kMT = k16 ? 2 : k84 ? 4 : 2;
+  static constexpr int kStages = stages(kWarps, kMT, kExtra);
+  static_assert(kStages >= 2, "a ring of two stages");
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kStage = stage(kMT);
+  static constexpr int kScaleAt = kMT * 2 * kCoreBytes + kActBytes;
+  static constexpr int kActAt = kMT * 2 * kCoreBytes;
+  static constexpr int kPitch = pitch(kMT);
+  static constexpr int kRed = NT * 8 * kPitch;  // floats of one warp's part
+  static constexpr int kRingAt = kStreamHead;
+  static constexpr int kRedAt = kRingAt + kWarps * kStages * kStage;
+  static constexpr int kExtraAt = kRedAt + red(kWarps, kMT);
+  static constexpr size_t kSmem = kExtraAt + kExtra;
+};
+
+// One warp's ring.
+template <typename S>
+struct Ring {
+  uint32_t buf, bar;
+  int put = 0, got = 0;  // stages asked for and taken
+  __device__ void init(uint32_t sbase, int warp, int lane) {
+    buf = sbase + S::kRingAt + warp * S::kStages * S::kStage;
+    bar = sbase + warp * S::kStages * 8;
+    if (lane < S::kStages) mbar_init(bar + lane * 8, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+  }
+  __device__ uint32_t next_buf() const { return buf + (put % S::kStages) * S::kStage; }
+  __device__ uint32_t next_bar() const { return bar + (put % S::kStages) * 8; }
+  __device__ bool wait(uint32_t* at) {
+    const int s = got % S::kStages;
+    *at = buf + s * S::kStage;
+    const bool ok = mbar_wait(bar + s * 8, (got / S::kStages) & 1);
+    ++got;
+    return ok;
+  }
+};
+
+// A fragments of one 16-row tile and K block (two cores in shared memory) times
+// the B fragments of NT column tiles, `live` of them in use, added to c.
+// k-step s takes the lane's elements 4 s .. 4 s + 3.
+template <int WK, int NT, int PARTS, int KS>
+__device__ __forceinline__ void mma_tile(uint32_t tile, int g, int q, const uint32_t (&b)[PARTS][NT][KS][2], int live,
+                                         float (&c)[NT][4]) {
+  const uint32_t r = tile + g * 128;
+  const uint32_t c0 = (uint32_t)(((2 * q) ^ g) << 4), c1 = (uint32_t)(((2 * q + 1) ^ g) << 4);
+  const uint4 v0 = lds128(r + c0), v1 = lds128(r + c1), v2 = lds128(r + kCoreBytes + c0), v3 = lds128(r + kCoreBytes + c1);
+  const uint32_t lo[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+  const uint32_t hi[8] = {v2.x, v2.y, v2.z, v2.w, v3.x, v3.y, v3.z, v3.w};
+#pragma unroll
+  for (int s = 0; s < KS; ++s) {
+    uint32_t a0, a1, a2, a3;
+    if constexpr (WK == kWE4M3) {
+      e4m3x4_to_half2(lo[s], a0, a2);
+      e4m3x4_to_half2(hi[s], a1, a3);
+    } else {
+      a0 = lo[2 * s];
+      a2 = lo[2 * s + 1];
+      a1 = hi[2 * s];
+      a3 = hi[2 * s + 1];
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if (NT > 1 && t >= live) break;
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p) mma16<WK == kWBF16>(c[t], a0, a1, a2, a3, b[p][t][s][0], b[p][t][s][1]);
+    }
+  }
+}
+
+// B fragments of one column tile from e4m3 rows in the stage: `left` bytes of
+// the K block exist, the rest counts as zero; rows beyond `rows` too.
+__device__ __forceinline__ void act_e4m3(uint32_t row, int q, bool there, int left, uint32_t (&b)[8][2]) {
+  uint32_t u[8] = {};
+  if (there) {
+    const uint4 v0 = lds128(row + 32 * q), v1 = lds128(row + 32 * q + 16);
+    u[0] = v0.x, u[1] = v0.y, u[2] = v0.z, u[3] = v0.w, u[4] = v1.x, u[5] = v1.y, u[6] = v1.z, u[7] = v1.w;
+  }
+  if (left < 128) {
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const int l = left - (32 * q + 4 * s);
+      u[s] &= l >= 4 ? ~0u : l <= 0 ? 0u : (1u << (8 * l)) - 1;
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < 8; ++s) e4m3x4_to_half2(u[s], b[s][0], b[s][1]);
+}
+
+}  // namespace effort
