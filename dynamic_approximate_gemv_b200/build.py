@@ -14,7 +14,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libeffort.so")
 LIB_DEBUG = os.path.join(HERE, "libeffort_debug.so")
 SOURCES = ["api.cu", "prep.cu", "effort.cu", "dense.cu", "noalloc.cu",
-           "api_ffn.cu", "norm.cu", "fp8.cu", "moe.cu"]
+           "api_ffn.cu", "norm.cu", "fp8.cu", "fp8_tc.cu", "tensor_map.cu", "moe.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = [

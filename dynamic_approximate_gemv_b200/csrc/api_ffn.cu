@@ -193,8 +193,9 @@ effort_status_t effort_moe_prepare(const effort_moe_weights_t* weights, void* st
     return EFFORT_ERR_UNSUPPORTED;
   const int E = a.n_experts, I = (int)a.in_dim, F = (int)a.hidden_dim, wk = (int)a.weight_kind;
   const int ke = k_per_block(wk);
-  const TileMat w13 = {nullptr, 2 * cdiv(F, 8), cdiv(I, ke), (size_t)2 * cdiv(F, 8) * cdiv(I, ke) * kCoreBytes};
-  const TileMat w2 = {nullptr, cdiv(I, 8), cdiv(F, ke), (size_t)cdiv(I, 8) * cdiv(F, ke) * kCoreBytes};
+  const int c13 = cdiv(2 * cdiv(F, 8), kGroupCores) * kGroupCores, c2 = cdiv(I, 8 * kGroupCores) * kGroupCores;
+  const TileMat w13 = {nullptr, c13, cdiv(I, ke), (size_t)c13 * cdiv(I, ke) * kCoreBytes};
+  const TileMat w2 = {nullptr, c2, cdiv(F, ke), (size_t)c2 * cdiv(F, ke) * kCoreBytes};
   const size_t scale_n = (size_t)E * cdiv(I, kBlk) * cdiv(F, kBlk);
   const size_t sbytes = q ? align_up(scale_n * 4, 256) : 0;
   const size_t rbytes = a.router ? align_up((size_t)E * I * dtype_size(a.router_dtype), 256) : 0;

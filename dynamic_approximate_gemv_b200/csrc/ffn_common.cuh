@@ -3,14 +3,17 @@
 //
 // Weight matrices are stored transposed ("rows" are output columns, K runs
 // along the input) and cut into cores of 8 rows x 128 bytes of K (128 e4m3
-// or 64 16-bit values), 1 KB each, in the order [matrix][row / 8][K block].
-// The K blocks of 8 rows are therefore one contiguous stream, which is what a
-// product with few tokens reads, and eight or sixteen cores of one K block
-// make the operand tile of a tensor-core product.  Inside a core, the 16-byte
+// or 64 16-bit values), 1 KB each, in the order [matrix][row / 64][K block]
+// [row / 8 % 8].  A block that walks along K reads one contiguous stream, 8 KB
+// for each K block of 64 rows (with the K blocks of 8 rows together instead,
+// blocks in step met the same memory channels and a stream ended at a third
+// of the bandwidth), and one or two such groups are the operand tile of a
+// tensor-core product as they are.  Inside a core, the 16-byte
 // chunk c of row r lies at chunk c ^ r (the 128-byte swizzle): a warp's 16-byte
 // reads of eight rows meet no shared-memory bank twice, and the tensor core
 // takes the tile as it is.  Rows and K are padded with zeros.
 #pragma once
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -40,13 +43,25 @@ __device__ __forceinline__ int core_offset(int r, int k, int esz) {
   return r * 128 + ((((b >> 4) ^ r) & 7) << 4) + (b & 15);
 }
 
+constexpr int kGroupCores = 8;       // cores that lie together
+constexpr int kGroupBytes = kGroupCores * kCoreBytes;
+// offset of a core in a matrix of nkb K blocks
+__host__ __device__ inline size_t core_at(int core, int kb, int nkb) {
+  return ((size_t)(core / kGroupCores) * nkb + kb) * kGroupBytes + (core % kGroupCores) * kCoreBytes;
+}
+
 // One stored matrix, or a stack of them.
 struct TileMat {
   const uint8_t* data;
-  int cores;           // 8-row groups of one matrix
+  int cores;           // 8-row groups of one matrix, a multiple of kGroupCores
   int nkb;             // K blocks
   size_t stride;       // bytes from one matrix of the stack to the next
 };
+
+// Tensor maps (tensor_map.cu).  False where the driver refuses.
+// Rows of bytes as {byte, row}: a copy brings 128 bytes of `box` rows in the
+// 128-byte swizzle; bytes and rows outside read as zero.
+bool map_rows(CUtensorMap* map, const void* data, long long bytes, long long rows, long long stride, int box);
 
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }

@@ -3,6 +3,7 @@
 //   out[r][n] = sum_b xs[r][b] ws[b][n / 128] sum_{k in b} x[r][k] w[k][n]
 //
 // and the layout of its weights.
+#include <stdlib.h>
 #include <atomic>
 
 #include "../../include/effort.h"
@@ -41,7 +42,7 @@ __global__ void __launch_bounds__(256) k_tile_weights(const T* __restrict__ w, i
 #pragma unroll
     for (int j = 0; j < (int)(16 / sizeof(T)); ++j) v[j] = t[ch * (16 / sizeof(T)) + j][c];
     const int r = col % 8;
-    *reinterpret_cast<uint4*>(out + mat * stride + ((size_t)core * nkb + kb) * kCoreBytes + r * 128 + ((ch ^ r) << 4)) =
+    *reinterpret_cast<uint4*>(out + mat * stride + core_at(core, kb, nkb) + r * 128 + ((ch ^ r) << 4)) =
         *reinterpret_cast<const uint4*>(v);
   }
 }
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(StreamShape<NT, 128>::kThreads, 1) k_fp8_few_r
     if (lane == 0) mbar_expect(bar, n * 2 * kCoreBytes + a.rows * xb + 16 + 16 * two);
     __syncwarp();
     if (lane < 2 * n)
-      bulk_load(buf + lane * kCoreBytes, a.w.data + ((size_t)(2 * t + lane) * a.w.nkb + kb) * kCoreBytes, kCoreBytes, bar);
+      bulk_load(buf + lane * kCoreBytes, a.w.data + core_at(2 * t + lane, kb, a.w.nkb), kCoreBytes, bar);
     else if (lane >= 30 - two && lane < 31)
       bulk_load(buf + S::kScaleAt + 16 * (30 - lane), a.ws + (size_t)(t / 8 + 30 - lane) * a.nkb4 + (kb & ~3), 16, bar);
   };
@@ -326,9 +327,15 @@ static cudaError_t launch_few_rows(FewRows a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, k_fp8_few_rows<NT>, a);
 }
 
+cudaError_t launch_fp8_tc(const TileMat& w, const float* ws, int I, int O, const uint8_t* x, int64_t xstride,
+                          const float* xs, int64_t xsstride, int64_t rows, int odt, void* out, int64_t ostride,
+                          cudaStream_t s);
+
 cudaError_t launch_fp8_matmul(const TileMat& w, const float* ws, int I, int O, const uint8_t* x, int64_t xstride,
                               const float* xs, int64_t xsstride, int64_t rows, int odt, void* out, int64_t ostride,
                               cudaStream_t s) {
+  if (rows > (getenv("XTC") ? atoi(getenv("XTC")) : 16))
+    return launch_fp8_tc(w, ws, I, O, x, xstride, xs, xsstride, rows, odt, out, ostride, s);
   const size_t osz = odt == kF32 ? 4 : 2;
   // 16 rows' scales of a very long K do not fit beside the ring: 8 rows then
   const int most = w.nkb > 1536 ? 8 : kFewRowsMax;

@@ -1,0 +1,563 @@
+// The product with e4m3 operands on the tensor cores (tcgen05):
+//
+//   out[r][n] = sum_b xs[r][b] ws[b][n / 128] sum_{k in b} x[r][k] w[k][n]
+//
+// Each K block of 128 is one accumulation of four matrix instructions in tensor
+// memory; the epilogue warps read it, multiply by the block's scales and add
+// it in fp32 registers while the next blocks are multiplied.
+//
+// Which operand takes the instruction's M side (the lanes of tensor memory):
+// for few rows the weights, so that x needs only N = 16, 32 or 64 columns;
+// else the rows of x, so that an epilogue thread holds one row and needs one
+// scale for each K block (with the weights there it needs one for each column:
+// 2300 clocks a K block of 128 x 256 against the instruction's 512).
+//
+// Roles: warp 0 copies (the weights' cores as they are stored, x through a
+// tensor map), warp 1 issues the matrix instructions, warp 2 turns the scales
+// of eight K blocks at a time into a table in shared memory (a row's scale
+// times the weight block's), the other warps are the epilogue.
+//
+// Work: the units are (tile, K block), tile after tile.  A cluster takes a
+// contiguous share of whole tiles and its blocks even, contiguous shares of
+// the cluster's units, so a block has whole tiles, which it stores, and a part
+// of its first and last tile.  Those parts are joined through distributed
+// shared memory once, at the end, in the blocks' order: no scratch, and the
+// same result every time.
+#include <stdlib.h>
+#include <atomic>
+#include <type_traits>
+
+#include "../../include/effort.h"
+#include "ffn_common.cuh"
+#include "stream.cuh"
+
+namespace effort {
+
+struct TcArgs {
+  TileMat w;
+  const float* ws;  // [out block][K block], rows of nkb4
+  int nkb4, O;
+  long long rows;
+  const float* xs;
+  long long xsstride;
+  void* out;
+  long long ostride;
+  int odt, ots, tiles, cluster;  // ots: tiles along the output columns
+};
+
+// ROWS: x on the M side.
+template <bool ROWS, int M, int N>
+struct TcShape {
+  static constexpr int kABytes = M * 128, kBBytes = N * 128;
+  static constexpr int kTileRows = ROWS ? M : N, kTileCols = ROWS ? N : M;  // of the output
+  static constexpr int kStage = kABytes + kBBytes;
+  static constexpr int kEpiWarps = ROWS ? 8 : 4;
+  static constexpr int kThreads = (3 + kEpiWarps) * 32 + 32;  // warp 3 is idle: the epilogue starts at a multiple of 4
+  // Accumulators in tensor memory, and the steps a K block is multiplied in: 256
+  // columns go in two, so that four accumulators fit and the epilogue has three
+  // steps' time to read one (with two of 256 columns the products waited for it).
+  static constexpr int kSteps = N == 256 ? 2 : 1, kStepN = N / kSteps;
+  static constexpr int kAcc = kStepN == 128 ? 4 : 8;
+  static constexpr int kTmemCols = kAcc * kStepN;
+  static constexpr int kSets = kEpiWarps / 4, kCols = kStepN / kSets;  // of one epilogue thread in one step
+  static constexpr int kBatch = 8, kBatches = 3;              // K blocks whose scales are turned at once
+  static constexpr bool kJoins = N <= 128;
+  static constexpr int kHead = 1024;
+  // the table of scales of one K block: for ROWS each row's for the 128 columns
+  // of each half, else each row's
+  static constexpr int kScales = ROWS ? M * (N / 128) : N;
+  static constexpr int kScaleBytes = kBatches * kBatch * kScales * 4;
+  static constexpr int kPitch = ROWS ? M + 1 : M;  // floats from one column of a part to the next
+  static constexpr int kPart = kPitch * N * 4, kJoinBytes = kJoins ? (kPart + 15) / 16 * 16 : 0;
+  static constexpr int kFree = kSmemMax - kHead - kScaleBytes - kJoinBytes;
+  static constexpr int kStages = kFree / kStage > 12 ? 12 : kFree / kStage;
+  static constexpr int kScaleAt = kHead + kStages * kStage, kJoinAt = kScaleAt + kScaleBytes;
+  static constexpr size_t kSmem = kJoinAt + kJoinBytes;
+  // parts to join: the first tile's has its own place, the last tile's is
+  // written when every stage has been used and lies over them
+  __host__ __device__ static constexpr int part(int slot) { return slot == 0 ? kJoinAt : kHead; }
+  static_assert(kStages >= 3 && (!kJoins || kPart <= kStages * kStage) && kSmem <= kSmemMax && kTmemCols <= 512, "fits");
+};
+
+// a descriptor of a K-major operand tile in the 128-byte swizzle, 8-row groups 1 KB apart
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
+  return (uint64_t)((addr & 0x3ffff) >> 4) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// One lane of a warp issues, but the whole warp runs the loop around it: the
+// instruction takes its operands from uniform registers, which a loop of one
+// lane would have to move there one by one.
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t e;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(e));
+  return e;
+}
+// ADD: to what the accumulator holds
+template <bool ADD>
+__device__ __forceinline__ void mma_f8(uint32_t e, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.b32 q, %5, 0; setp.ne.b32 p, %4, 0;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "n"(ADD ? 1 : 0), "r"(e)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t e, uint32_t bar) {
+  asm volatile(
+      "{ .reg .pred q; setp.ne.b32 q, %1, 0;\n"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar), "r"(e)
+      : "memory");
+}
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tensor_load2(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+// 16 columns of this warp's 32 lanes
+__device__ __forceinline__ void tmem_load16(uint32_t at, float (&v)[16]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at));
+}
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// A wait that gives up at once after the block's first failure.
+__device__ __forceinline__ void tc_wait(uint32_t bar, uint32_t parity, bool& fine) {
+  if (fine) fine = mbar_wait(bar, parity);
+}
+
+// One thread's accumulators to the output: for ROWS C columns of one row, else
+// one column of C rows.
+template <bool ROWS, int C>
+__device__ __forceinline__ void store_tile(const TcArgs& a, const float (&acc)[C], long long r0, int c0) {
+  auto put = [&](auto* o) {
+    using T = std::remove_pointer_t<decltype(o)>;
+    if constexpr (ROWS) {
+      if (r0 >= a.rows) return;
+      T* p = o + r0 * a.ostride + c0;
+      const int live = a.O - c0;
+      if (live >= C && ((uintptr_t)p & 15) == 0) {
+        constexpr int V = 16 / sizeof(T);
+#pragma unroll
+        for (int j = 0; j < C; j += V) {
+          alignas(16) T v[V];
+#pragma unroll
+          for (int i = 0; i < V; ++i) v[i] = from_float<T>(acc[j + i]);
+          *reinterpret_cast<uint4*>(p + j) = *reinterpret_cast<const uint4*>(v);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+          if (j < live) p[j] = from_float<T>(acc[j]);
+      }
+    } else {
+      if (c0 >= a.O) return;
+      T* p = o + r0 * a.ostride + c0;
+      const int live = (int)min((long long)C, a.rows - r0);
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+        if (j < live) p[j * a.ostride] = from_float<T>(acc[j]);
+    }
+  };
+  if (a.odt == kF32) put((float*)a.out);
+  else if (a.odt == kF16) put((__half*)a.out);
+  else put((__nv_bfloat16*)a.out);
+}
+
+// Steps through a block's units without a division each.
+struct Walk {
+  int kb, ot, tt;  // K block, output-column tile, row tile
+  __device__ Walk(int tile, int kb_, int ots) : kb(kb_), ot(tile % ots), tt(tile / ots) {}
+  __device__ void step(int nkb, int ots) {
+    if (++kb == nkb) {
+      kb = 0;
+      if (++ot == ots) {
+        ot = 0;
+        ++tt;
+      }
+    }
+  }
+};
+
+template <bool ROWS, int M, int N>
+__global__ void __launch_bounds__(TcShape<ROWS, M, N>::kThreads, 1)
+    k_fp8_tc(const __grid_constant__ CUtensorMap xmap, const TcArgs a) {
+  using S = TcShape<ROWS, M, N>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cl = a.cluster, rank = cl > 1 ? (int)cluster_rank() : 0;
+  const int ncl = gridDim.x / cl, c = blockIdx.x / cl;
+  const int T0 = (int)((long long)a.tiles * c / ncl), T1 = (int)((long long)a.tiles * (c + 1) / ncl);
+  const int nkb = a.w.nkb;
+  // where each block of the cluster starts: its tile (from T0 on) and K block
+  const long long units = (long long)(T1 - T0) * nkb;
+  const long long u0 = units * rank / cl, u1 = units * (rank + 1) / cl;
+  const int mine = (int)(u1 - u0);
+  const Walk start(T0 + (int)(u0 / nkb), (int)(u0 % nkb), a.ots);
+
+  // barriers: stage full / free, accumulator full / read, scales full / read
+  const uint32_t b_full = sbase, b_free = b_full + 8 * S::kStages, b_accf = b_free + 8 * S::kStages,
+                 b_acce = b_accf + 8 * S::kAcc, b_scf = b_acce + 8 * S::kAcc, b_sce = b_scf + 8 * S::kBatches,
+                 tmem_at = b_sce + 8 * S::kBatches;
+  volatile int* bad = reinterpret_cast<volatile int*>(smem + (tmem_at + 8 - sbase));  // some wait ran out
+  int2* from = reinterpret_cast<int2*>(smem + S::kHead - 9 * sizeof(int2));
+  if (threadIdx.x >= 32 && threadIdx.x <= 32 + cl) {
+    const long long u = units * (threadIdx.x - 32) / cl;
+    from[threadIdx.x - 32] = make_int2((int)(u / nkb), (int)(u % nkb));
+  }
+  if (threadIdx.x == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&xmap) : "memory");
+    *bad = 0;
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(b_full + 8 * i, 1);
+      mbar_init(b_free + 8 * i, 1);
+    }
+    for (int i = 0; i < S::kAcc; ++i) {
+      mbar_init(b_accf + 8 * i, 1);
+      mbar_init(b_acce + 8 * i, S::kEpiWarps);
+    }
+    for (int i = 0; i < S::kBatches; ++i) {
+      mbar_init(b_scf + 8 * i, 1);
+      mbar_init(b_sce + 8 * i, S::kEpiWarps);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tmem_at), "n"(S::kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = *reinterpret_cast<const uint32_t*>(smem + (tmem_at - sbase));
+  bool fine = true;
+  // the widest shape: 384 threads launched with 168 registers; 8 x 32 x 208 + 4 x
+  // 32 x 80 fit in them
+  if constexpr (N == 256) {
+    static_assert(256 * 208 + 128 * 80 <= 384 * 168, "within the block's registers");
+  }
+
+  if (warp < 4) {
+  if constexpr (N == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------ copies
+    // (one lane: the copies take their operands from the warp's uniform registers)
+    const int last_group = a.w.cores / kGroupCores - 1;  // columns behind it are not stored: any weights do
+    auto load_w = [&](const Walk& w, int s) {
+      mbar_expect(b_full + 8 * s, S::kStage);
+#pragma unroll
+      for (int h = 0; h < S::kTileCols / 64; ++h)
+        bulk_load(sbase + S::kHead + s * S::kStage + (ROWS ? S::kABytes : 0) + h * kGroupBytes,
+                  a.w.data + core_at(min(w.ot * (S::kTileCols / 64) + h, last_group) * kGroupCores, w.kb, nkb), kGroupBytes,
+                  b_full + 8 * s);
+    };
+    auto load_x = [&](const Walk& w, int s) {
+      tensor_load2(sbase + S::kHead + s * S::kStage + (ROWS ? 0 : S::kABytes), &xmap, w.kb * kBlk, w.tt * S::kTileRows,
+                   b_full + 8 * s);
+    };
+    // the first stages' weights do not depend on the kernel before
+    const int early = min(S::kStages, mine);
+    Walk w = start, x = start;
+    for (int i = 0; i < early; ++i, w.step(nkb, a.ots)) load_w(w, i);
+    grid_dep_wait();
+    for (int i = 0; i < early; ++i, x.step(nkb, a.ots)) load_x(x, i);
+    int s = 0, ph = 0;
+    if (early == S::kStages)
+      for (int n = early; n < mine; ++n, w.step(nkb, a.ots)) {
+        tc_wait(b_free + 8 * s, ph, fine);
+        load_w(w, s);
+        load_x(w, s);
+        if (++s == S::kStages) s = 0, ph ^= 1;
+      }
+  } else if (warp == 1) {
+    // ------------------------------------------------ matrix instructions
+    // fp32 sums, e4m3 operands, both K-major, N and M
+    constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(S::kStepN >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+    const uint64_t a0 = smem_desc(sbase + S::kHead);
+    const uint32_t e = elect();
+    int s = 0, ph = 0, as = 0, aph = 1;  // aph: an accumulator's first use waits for nothing
+    for (int n = 0; n < mine; ++n) {
+      // the stage and the K block's accumulators (kAcc is a multiple of kSteps)
+      const uint32_t f = b_full + 8 * s, r = b_acce + 8 * as;
+      bool ready;
+      if constexpr (S::kSteps == 2) ready = mbar_try3(f, ph, r, aph, r + 8, aph);
+      else ready = mbar_try2(f, ph, r, aph);
+      if (!ready) {
+        tc_wait(f, ph, fine);
+#pragma unroll
+        for (int h = 0; h < S::kSteps; ++h) tc_wait(r + 8 * h, aph, fine);
+      }
+      tc_after();
+      const uint64_t da = a0 + (uint64_t)(s * (S::kStage >> 4)), db = da + (S::kABytes >> 4);
+#pragma unroll
+      for (int h = 0; h < S::kSteps; ++h) {
+        const uint64_t dh = db + (uint64_t)(h * S::kStepN * 128 >> 4);
+        const uint32_t d = tmem + (as + h) * S::kStepN;
+        mma_f8<false>(e, d, da, dh, idesc);
+#pragma unroll
+        for (int k = 1; k < 4; ++k) mma_f8<true>(e, d, da + 2 * k, dh + 2 * k, idesc);
+        mma_commit(e, b_accf + 8 * (as + h));
+      }
+      mma_commit(e, b_free + 8 * s);
+      as += S::kSteps;
+      if (as == S::kAcc) as = 0, aph ^= 1;
+      if (++s == S::kStages) s = 0, ph ^= 1;
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------ scales
+    grid_dep_launch();
+    grid_dep_wait();
+    constexpr int R = (S::kTileRows + 31) / 32, H = S::kScales / S::kTileRows;  // rows of a lane, halves
+    int batch = 0;
+    Walk at = start;
+    for (int u = 0; u < mine; ++batch) {
+      const int kb = at.kb, n = min(min(S::kBatch, nkb - kb), mine - u), sl = batch % S::kBatches;
+      float v[R][S::kBatch], w[H][S::kBatch];
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        // a tile's last half may lie behind the last block of columns
+        const float* pw = a.ws + (size_t)min(at.ot * S::kTileCols / kBlk + h, (a.O - 1) / kBlk) * a.nkb4 + kb;
+#pragma unroll
+        for (int k = 0; k < S::kBatch; ++k) w[h][k] = k < n ? __ldg(pw + k) : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const long long r = (long long)at.tt * S::kTileRows + 32 * i + lane;
+        const bool there = 32 * i + lane < S::kTileRows && r < a.rows;
+        const float* p = a.xs + (there ? r : 0) * a.xsstride + kb;
+#pragma unroll
+        for (int k = 0; k < S::kBatch; ++k) v[i][k] = there && k < n ? __ldg(p + k) : 0.0f;
+      }
+      if (batch >= S::kBatches) tc_wait(b_sce + 8 * sl, (batch / S::kBatches - 1) & 1, fine);
+      float* t = reinterpret_cast<float*>(smem + S::kScaleAt) + sl * S::kBatch * S::kScales;
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int k = 0; k < S::kBatch; ++k)
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+            if (32 * i + lane < S::kTileRows) t[k * S::kScales + h * S::kTileRows + 32 * i + lane] = v[i][k] * w[h][k];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_scf + 8 * sl);
+      u += n;
+      at.kb += n - 1;
+      at.step(nkb, a.ots);
+    }
+  }
+  } else {
+    // ------------------------------------------------ epilogue
+    if constexpr (N == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int quarter = warp & 3, set = (warp - 4) >> 2;
+    const int row = quarter * 32 + lane;  // lane of tensor memory
+    const uint32_t tm = tmem + ((uint32_t)(quarter * 32) << 16) + set * S::kCols;
+    float acc[S::kSteps][S::kCols];
+    int batch = -1, bi = 0, bn = 0;  // the batch of scales in use, the K block in it, and how many it has
+    int kb_first = 0;                // first K block of the current tile that is this block's
+    Walk w = start;
+    bool first_tile = true;
+    int as = 0, aph = 0;
+    for (int n = 0; n < mine; ++n) {
+      const int kb = w.kb;
+      if (n == 0 || kb == 0) {
+        kb_first = kb;
+#pragma unroll
+        for (int h = 0; h < S::kSteps; ++h)
+#pragma unroll
+          for (int j = 0; j < S::kCols; ++j) acc[h][j] = 0.0f;
+      }
+      if (bi == bn) {
+        ++batch;
+        bi = 0;
+        bn = min(min(S::kBatch, nkb - kb), mine - n);
+        tc_wait(b_scf + 8 * (batch % S::kBatches), (batch / S::kBatches) & 1, fine);
+      }
+      const uint32_t sc = sbase + S::kScaleAt + (uint32_t)(((batch % S::kBatches) * S::kBatch + bi) * S::kScales) * 4;
+#pragma unroll
+      for (int h = 0; h < S::kSteps; ++h) {
+        // pieces of the columns: the next one is on its way while one is added
+        constexpr int kPiece = S::kCols < 32 ? 16 : 32, kPieces = S::kCols / kPiece;
+        float one = 0.0f;                // ROWS: the row's scale
+        uint4 f[ROWS ? 1 : kPiece / 4];  // else: a piece's, one for each column
+        if constexpr (ROWS) one = lds_float(sc + (h * M + row) * 4);
+        else {
+#pragma unroll
+          for (int j = 0; j < kPiece / 4; ++j) f[j] = lds128(sc + 16 * j);
+        }
+        tc_wait(b_accf + 8 * as, aph, fine);
+        tc_after();
+        const uint32_t at = tm + as * S::kStepN, read = b_acce + 8 * as;
+        as = as + 1 == S::kAcc ? 0 : as + 1;
+        aph ^= as == 0;
+        float v[2][kPiece / 16][16];
+#pragma unroll
+        for (int i = 0; i < kPiece / 16; ++i) tmem_load16(at + 16 * i, v[0][i]);
+#pragma unroll
+        for (int pc = 0; pc < kPieces; ++pc) {
+          tmem_wait();
+          if (pc + 1 == kPieces) {  // the accumulator may be written again
+            tc_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(read);
+          } else {
+#pragma unroll
+            for (int i = 0; i < kPiece / 16; ++i) tmem_load16(at + (pc + 1) * kPiece + 16 * i, v[(pc + 1) & 1][i]);
+          }
+#pragma unroll
+          for (int j = 0; j < kPiece; j += 4) {
+            const uint4 g = ROWS ? make_uint4(0, 0, 0, 0) : f[ROWS ? 0 : j / 4];
+            float* d = acc[h] + pc * kPiece + j;
+            const float* x = &v[pc & 1][j / 16][j % 16];
+            d[0] = fmaf(x[0], ROWS ? one : __uint_as_float(g.x), d[0]);
+            d[1] = fmaf(x[1], ROWS ? one : __uint_as_float(g.y), d[1]);
+            d[2] = fmaf(x[2], ROWS ? one : __uint_as_float(g.z), d[2]);
+            d[3] = fmaf(x[3], ROWS ? one : __uint_as_float(g.w), d[3]);
+          }
+          if constexpr (!ROWS) {
+            if (pc + 1 < kPieces) {
+#pragma unroll
+              for (int j = 0; j < kPiece / 4; ++j) f[j] = lds128(sc + 4 * (pc + 1) * kPiece + 16 * j);
+            }
+          }
+        }
+      }
+      if (++bi == bn) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_sce + 8 * (batch % S::kBatches));
+      }
+      if (kb == nkb - 1 || n + 1 == mine) {
+        const float poison = !fine || *bad ? __int_as_float(0x7fffffff) : 0.0f;
+        const bool whole = kb_first == 0 && kb == nkb - 1;
+        float* part = reinterpret_cast<float*>(smem + S::part(first_tile ? 0 : 1));
+#pragma unroll
+        for (int h = 0; h < S::kSteps; ++h) {
+          const int c0 = h * S::kStepN + set * S::kCols;  // first N-side column of this thread
+#pragma unroll
+          for (int j = 0; j < S::kCols; ++j) acc[h][j] += poison;
+          if (whole)
+            store_tile<ROWS, S::kCols>(a, acc[h], (long long)w.tt * S::kTileRows + (ROWS ? row : c0),
+                                       w.ot * S::kTileCols + (ROWS ? c0 : row));
+          else if (S::kJoins) {
+#pragma unroll
+            for (int j = 0; j < S::kCols; ++j) part[(c0 + j) * S::kPitch + row] = acc[h][j];
+          }
+        }
+        first_tile = false;
+      }
+      w.step(nkb, a.ots);
+    }
+  }
+  if (!fine) *bad = 1;
+  __syncwarp();
+  if (warp != 2) grid_dep_launch();
+  tc_before();
+  __syncthreads();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kTmemCols));
+  if (!S::kJoins || cl == 1) return;
+  cluster_sync();
+  for (int i = 1; i < cl; ++i) {
+    // the tile that block i starts in the middle of, if it is the first to
+    const int t = from[i].x;
+    if (from[i].y == 0 || (from[i - 1].x == t && from[i - 1].y != 0)) continue;
+    int last = i;  // blocks i - 1 .. last have a part of it
+    while (last + 1 < cl && from[last + 1].x == t) ++last;
+    const int tile = T0 + t, ot = tile % a.ots, tt = tile / a.ots;
+    // neighbouring threads take neighbouring output columns
+    const int live = (int)min((long long)S::kTileRows, a.rows - (long long)tt * S::kTileRows);
+    for (int e = rank * (int)blockDim.x + threadIdx.x; e < live * S::kTileCols; e += cl * (int)blockDim.x) {
+      const int r = e / S::kTileCols, o = e % S::kTileCols, col = ot * S::kTileCols + o;
+      const uint32_t at = (uint32_t)(ROWS ? o * S::kPitch + r : r * S::kPitch + o) * 4;
+      float s = 0.0f;
+      for (int b = i - 1; b <= last; ++b) s += remote_float(sbase + S::part(from[b].x == t ? 0 : 1) + at, b);
+      if (col < a.O) store_dt(a.out, a.odt, ((long long)tt * S::kTileRows + r) * a.ostride + col, s);
+    }
+  }
+  cluster_sync();  // no block leaves while its parts are read
+}
+
+// ---------------------------------------------------------------- host
+template <bool ROWS, int M, int N>
+static cudaError_t launch_tc(const TileMat& w, const float* ws, int I, int O, const uint8_t* x, int64_t xstride,
+                             const float* xs, int64_t xsstride, int64_t rows, int odt, void* out, int64_t ostride,
+                             cudaStream_t s) {
+  using S = TcShape<ROWS, M, N>;
+  static std::atomic<int> fit[kMaxDevices][4];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(S::kThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = s;
+  cfg.attrs = at;
+  if (fit[dev][0].load() == 0) {
+    e = cudaFuncSetAttribute(k_fp8_tc<ROWS, M, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+    if (e != cudaSuccess) return e;
+    for (int i = 3; i >= 0; --i) {
+      at[0].val.clusterDim.x = 1u << i;
+      cfg.gridDim = dim3(1u << i);
+      cfg.numAttrs = 1;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, k_fp8_tc<ROWS, M, N>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+      }
+      fit[dev][i].store(n);
+    }
+    if (fit[dev][0].load() < 1) return cudaErrorLaunchOutOfResources;
+  }
+  const int ots = cdiv(O, S::kTileCols), nkb = w.nkb;
+  const long long tiles = (long long)ots * cdiv(rows, S::kTileRows);
+  if (tiles > 0x7fffffffll) return cudaErrorInvalidValue;
+  TcArgs a = {w, ws, align4(nkb), O, rows, xs, xsstride, out, ostride, odt, ots, (int)tiles, 1};
+  // the cluster size whose longest share of units is shortest; the join is
+  // counted as eight of them
+  long long best = 0;
+  int ncl = 0;
+  for (int i = 0; i < (S::kJoins ? 4 : 1); ++i) {
+    const long long cl = 1ll << i, n = fit[dev][i].load() < tiles ? fit[dev][i].load() : tiles;
+    if (n < 1 || cl > nkb) break;
+    const long long per = (tiles + n - 1) / n * nkb, cost = (per + cl - 1) / cl + (cl > 1 ? 8 : 0);
+    if (ncl == 0 || cost < best) {
+      best = cost;
+      a.cluster = (int)cl;
+      ncl = (int)n;
+    }
+  }
+  CUtensorMap xmap;
+  if (!map_rows(&xmap, x, I, rows, xstride, S::kTileRows)) return cudaErrorInvalidValue;
+  at[0].val.clusterDim.x = (unsigned)a.cluster;
+  cfg.gridDim = dim3((unsigned)(ncl * a.cluster));
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_fp8_tc<ROWS, M, N>, xmap, a);
+}
+
+cudaError_t launch_fp8_tc(const TileMat& w, const float* ws, int I, int O, const uint8_t* x, int64_t xstride,
+                          const float* xs, int64_t xsstride, int64_t rows, int odt, void* out, int64_t ostride,
+                          cudaStream_t s) {
+#define GO(ROWS, M, N) return launch_tc<ROWS, M, N>(w, ws, I, O, x, xstride, xs, xsstride, rows, odt, out, ostride, s)
+  if (rows <= 16) GO(false, 128, 16);
+  if (rows <= 32) GO(false, 128, 32);
+  if (rows <= (getenv("XR") ? atoi(getenv("XR")) : 64)) GO(false, 128, 64);
+  if ((long long)cdiv(O, 256) * cdiv(rows, 128) < 100) GO(true, 128, 128);
+  GO(true, 128, 256);
+#undef GO
+}
+
+}  // namespace effort

@@ -62,8 +62,8 @@ __global__ void __launch_bounds__(256) k_moe_up(MoeCall c) {
   const uint8_t* base = c.w13.data + e * c.w13.stride;
   float a = 0.0f, b = 0.0f;
   for (int kb = 0; kb < c.w13.nkb; ++kb) {
-    const uint8_t* c1 = base + ((size_t)(2 * (j / 8)) * c.w13.nkb + kb) * kCoreBytes;
-    const uint8_t* c3 = c1 + (size_t)c.w13.nkb * kCoreBytes;
+    const uint8_t* c1 = base + core_at(2 * (j / 8), kb, c.w13.nkb);
+    const uint8_t* c3 = base + core_at(2 * (j / 8) + 1, kb, c.w13.nkb);
     float da = 0.0f, db = 0.0f;
     for (int k = lane; k < ke; k += 32) {
       const int kk = kb * ke + k;
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(256) k_moe_down(MoeCall c) {
     const uint8_t* base = c.w2.data + e * c.w2.stride;
     float a = 0.0f;
     for (int kb = 0; kb < c.w2.nkb; ++kb) {
-      const uint8_t* core = base + ((size_t)(i / 8) * c.w2.nkb + kb) * kCoreBytes;
+      const uint8_t* core = base + core_at(i / 8, kb, c.w2.nkb);
       float d = 0.0f;
       for (int k = lane; k < ke; k += 32) {
         const int kk = kb * ke + k;
