@@ -107,8 +107,8 @@ __global__ void __launch_bounds__(StreamShape<NT, 128>::kThreads, 1) k_fp8_few_r
   const uint32_t sbase = smem_u32(smem);
   float* red = reinterpret_cast<float*>(smem + S::kRedAt);
   const uint32_t xtab = sbase + S::kExtraAt;  // x_scales of the block's K blocks: [K block][NT * 8]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-  const int cl = a.cluster, rank = cl > 1 ? (int)cluster_rank() : 0;
+  const int lane = threadIdx.x & 31, warp = warp_index(), g = lane >> 2, q = lane & 3;
+  const int cl = a.cluster, rank = cluster_rank();
   const int ncl = gridDim.x / cl, c = blockIdx.x / cl;
   const int t0 = (int)((long long)a.tiles * c / ncl), t1 = (int)((long long)a.tiles * (c + 1) / ncl);
   const int kb0 = a.w.nkb * rank / cl, kb1 = a.w.nkb * (rank + 1) / cl;

@@ -45,6 +45,7 @@ struct TcArgs {
   int odt, ots, tiles, cluster;  // ots: tiles along the output columns
 };
 
+constexpr int kTurn = 32 * 64;  // 64 bytes of 32 rows
 // ROWS: x on the M side.
 template <bool ROWS, int M, int N>
 struct TcShape {
@@ -60,19 +61,23 @@ struct TcShape {
   static constexpr int kAcc = kStepN == 128 ? 4 : 8;
   static constexpr int kTmemCols = kAcc * kStepN;
   static constexpr int kSets = kEpiWarps / 4, kCols = kStepN / kSets;  // of one epilogue thread in one step
-  static constexpr int kBatch = 8, kBatches = 3;              // K blocks whose scales are turned at once
+  static constexpr int kBatch = 8, kBatches = N == 256 ? 2 : 3;  // K blocks whose scales are turned at once
   static constexpr bool kJoins = N <= 128;
   static constexpr int kHead = 1024;
   // the table of scales of one K block: for ROWS each row's for the 128 columns
   // of each half, else each row's
   static constexpr int kScales = ROWS ? M * (N / 128) : N;
   static constexpr int kScaleBytes = kBatches * kBatch * kScales * 4;
-  static constexpr int kPitch = ROWS ? M + 1 : M;  // floats from one column of a part to the next
-  static constexpr int kPart = kPitch * N * 4, kJoinBytes = kJoins ? (kPart + 15) / 16 * 16 : 0;
-  static constexpr int kFree = kSmemMax - kHead - kScaleBytes - kJoinBytes;
+  // a part in shared memory: rows of the output, their columns together (the
+  // blocks of a cluster read it 16 bytes a lane); + 4 floats for the banks
+  static constexpr int kPitch = kTileCols + 4;
+  static constexpr int kPart = kTileRows * kPitch * 4, kJoinBytes = kJoins ? kPart : 0;
+  static constexpr int kTurnBytes = ROWS ? kEpiWarps * kTurn : 0;  // where a warp turns its rows to whole sectors
+  static constexpr int kFree = kSmemMax - kHead - kScaleBytes - kJoinBytes - kTurnBytes;
   static constexpr int kStages = kFree / kStage > 12 ? 12 : kFree / kStage;
-  static constexpr int kScaleAt = kHead + kStages * kStage, kJoinAt = kScaleAt + kScaleBytes;
-  static constexpr size_t kSmem = kJoinAt + kJoinBytes;
+  static constexpr int kScaleAt = kHead + kStages * kStage, kJoinAt = kScaleAt + kScaleBytes,
+                       kTurnAt = kJoinAt + kJoinBytes;
+  static constexpr size_t kSmem = kTurnAt + kTurnBytes;
   // parts to join: the first tile's has its own place, the last tile's is
   // written when every stage has been used and lies over them
   __host__ __device__ static constexpr int part(int slot) { return slot == 0 ? kJoinAt : kHead; }
@@ -136,23 +141,40 @@ __device__ __forceinline__ void tc_wait(uint32_t bar, uint32_t parity, bool& fin
 // One thread's accumulators to the output: for ROWS C columns of one row, else
 // one column of C rows.
 template <bool ROWS, int C>
-__device__ __forceinline__ void store_tile(const TcArgs& a, const float (&acc)[C], long long r0, int c0) {
+__device__ __forceinline__ void store_tile(const TcArgs& a, const float (&acc)[C], long long r0, int c0, uint4* turn) {
   auto put = [&](auto* o) {
     using T = std::remove_pointer_t<decltype(o)>;
     if constexpr (ROWS) {
-      if (r0 >= a.rows) return;
-      T* p = o + r0 * a.ostride + c0;
-      const int live = a.O - c0;
-      if (live >= C && ((uintptr_t)p & 15) == 0) {
-        constexpr int V = 16 / sizeof(T);
+      // A lane holds one row, and rows lie far apart: 64 bytes of the warp's 32
+      // rows at a time go through shared memory, so that four lanes write 64
+      // bytes of a row (16 bytes at a time from each lane alone were half
+      // sectors: 60 of 386 us at 4096 x 4096 x 14336).
+      constexpr int V = 16 / sizeof(T), P = 64 / sizeof(T);  // elements of 16 and of 64 bytes
+      const int lane = threadIdx.x & 31;
+      const bool wide = a.O - c0 >= C && (((uintptr_t)(o + c0) | (uintptr_t)(a.ostride * sizeof(T))) & 15) == 0;
+      if (wide) {
 #pragma unroll
-        for (int j = 0; j < C; j += V) {
-          alignas(16) T v[V];
+        for (int j = 0; j < C; j += P) {
+          __syncwarp();
 #pragma unroll
-          for (int i = 0; i < V; ++i) v[i] = from_float<T>(acc[j + i]);
-          *reinterpret_cast<uint4*>(p + j) = *reinterpret_cast<const uint4*>(v);
+          for (int q = 0; q < 4; ++q) {
+            alignas(16) T v[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = from_float<T>(acc[j + q * V + i]);
+            turn[lane * 4 + (q ^ ((lane >> 1) & 3))] = *reinterpret_cast<const uint4*>(v);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + (lane >> 2), q = lane & 3;
+            const long long rr = r0 - lane + r;
+            if (rr < a.rows)
+              *reinterpret_cast<uint4*>(o + rr * a.ostride + c0 + j + q * V) = turn[r * 4 + (q ^ ((r >> 1) & 3))];
+          }
         }
-      } else {
+      } else if (r0 < a.rows) {
+        T* p = o + r0 * a.ostride + c0;
+        const int live = a.O - c0;
 #pragma unroll
         for (int j = 0; j < C; ++j)
           if (j < live) p[j] = from_float<T>(acc[j]);
@@ -192,8 +214,8 @@ __global__ void __launch_bounds__(TcShape<ROWS, M, N>::kThreads, 1)
   using S = TcShape<ROWS, M, N>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cl = a.cluster, rank = cl > 1 ? (int)cluster_rank() : 0;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+  const int cl = a.cluster, rank = cluster_rank();
   const int ncl = gridDim.x / cl, c = blockIdx.x / cl;
   const int T0 = (int)((long long)a.tiles * c / ncl), T1 = (int)((long long)a.tiles * (c + 1) / ncl);
   const int nkb = a.w.nkb;
@@ -319,6 +341,7 @@ __global__ void __launch_bounds__(TcShape<ROWS, M, N>::kThreads, 1)
     grid_dep_launch();
     grid_dep_wait();
     constexpr int R = (S::kTileRows + 31) / 32, H = S::kScales / S::kTileRows;  // rows of a lane, halves
+    const bool vec = ((uintptr_t)a.xs & 15) == 0 && (a.xsstride & 3) == 0;
     int batch = 0;
     Walk at = start;
     for (int u = 0; u < mine; ++batch) {
@@ -336,8 +359,16 @@ __global__ void __launch_bounds__(TcShape<ROWS, M, N>::kThreads, 1)
         const long long r = (long long)at.tt * S::kTileRows + 32 * i + lane;
         const bool there = 32 * i + lane < S::kTileRows && r < a.rows;
         const float* p = a.xs + (there ? r : 0) * a.xsstride + kb;
+        if (vec && (kb & 3) == 0 && n == S::kBatch) {
 #pragma unroll
-        for (int k = 0; k < S::kBatch; ++k) v[i][k] = there && k < n ? __ldg(p + k) : 0.0f;
+          for (int k = 0; k < S::kBatch; k += 4) {
+            const float4 q = there ? __ldg(reinterpret_cast<const float4*>(p + k)) : make_float4(0, 0, 0, 0);
+            v[i][k] = q.x, v[i][k + 1] = q.y, v[i][k + 2] = q.z, v[i][k + 3] = q.w;
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < S::kBatch; ++k) v[i][k] = there && k < n ? __ldg(p + k) : 0.0f;
+        }
       }
       if (batch >= S::kBatches) tc_wait(b_sce + 8 * sl, (batch / S::kBatches - 1) & 1, fine);
       float* t = reinterpret_cast<float*>(smem + S::kScaleAt) + sl * S::kBatch * S::kScales;
@@ -362,82 +393,86 @@ __global__ void __launch_bounds__(TcShape<ROWS, M, N>::kThreads, 1)
     const int row = quarter * 32 + lane;  // lane of tensor memory
     const uint32_t tm = tmem + ((uint32_t)(quarter * 32) << 16) + set * S::kCols;
     float acc[S::kSteps][S::kCols];
-    int batch = -1, bi = 0, bn = 0;  // the batch of scales in use, the K block in it, and how many it has
-    int kb_first = 0;                // first K block of the current tile that is this block's
+    int slot = 0, sph = 0;  // batch of scales in use
     Walk w = start;
     bool first_tile = true;
     int as = 0, aph = 0;
-    for (int n = 0; n < mine; ++n) {
-      const int kb = w.kb;
-      if (n == 0 || kb == 0) {
-        kb_first = kb;
+    // The columns go in pieces, and the next piece is on its way (into the other
+    // half of v) while one is added, over the ends of steps and K blocks too.
+    constexpr int kPiece = S::kCols < 32 || N == 256 ? 16 : 32, kPieces = S::kCols / kPiece, kLoads = kPiece / 16;
+    static_assert(kPieces == 1 || kPieces % 2 == 0, "a step starts in the first half");
+    float v[2][kLoads][16];
+    auto open = [&]() {  // the next accumulator's first piece
+      tc_wait(b_accf + 8 * as, aph, fine);
+      tc_after();
 #pragma unroll
-        for (int h = 0; h < S::kSteps; ++h)
+      for (int i = 0; i < kLoads; ++i) tmem_load16(tm + as * S::kStepN + 16 * i, v[kPieces == 1][i]);
+    };
+    if (mine > 0) open();
+    for (int n = 0; n < mine;) {
+      // the rest of a tile, as far as it is this block's; its scales batch by batch
+      const int kb_first = w.kb, seg = min(nkb - kb_first, mine - n);
 #pragma unroll
-          for (int j = 0; j < S::kCols; ++j) acc[h][j] = 0.0f;
-      }
-      if (bi == bn) {
-        ++batch;
-        bi = 0;
-        bn = min(min(S::kBatch, nkb - kb), mine - n);
-        tc_wait(b_scf + 8 * (batch % S::kBatches), (batch / S::kBatches) & 1, fine);
-      }
-      const uint32_t sc = sbase + S::kScaleAt + (uint32_t)(((batch % S::kBatches) * S::kBatch + bi) * S::kScales) * 4;
+      for (int h = 0; h < S::kSteps; ++h)
 #pragma unroll
-      for (int h = 0; h < S::kSteps; ++h) {
-        // pieces of the columns: the next one is on its way while one is added
-        constexpr int kPiece = S::kCols < 32 ? 16 : 32, kPieces = S::kCols / kPiece;
-        float one = 0.0f;                // ROWS: the row's scale
-        uint4 f[ROWS ? 1 : kPiece / 4];  // else: a piece's, one for each column
-        if constexpr (ROWS) one = lds_float(sc + (h * M + row) * 4);
-        else {
+        for (int j = 0; j < S::kCols; ++j) acc[h][j] = 0.0f;
+      for (int b0 = 0; b0 < seg; b0 += S::kBatch) {
+        const int bn = min(S::kBatch, seg - b0);
+        tc_wait(b_scf + 8 * slot, sph, fine);
+        uint32_t sc = sbase + S::kScaleAt + slot * S::kBatch * S::kScales * 4 + (ROWS ? row * 4 : 0);
+        for (int i = 0; i < bn; ++i, sc += S::kScales * 4) {
+          const bool more = n + b0 + i + 1 < mine;
 #pragma unroll
-          for (int j = 0; j < kPiece / 4; ++j) f[j] = lds128(sc + 16 * j);
-        }
-        tc_wait(b_accf + 8 * as, aph, fine);
-        tc_after();
-        const uint32_t at = tm + as * S::kStepN, read = b_acce + 8 * as;
-        as = as + 1 == S::kAcc ? 0 : as + 1;
-        aph ^= as == 0;
-        float v[2][kPiece / 16][16];
+          for (int h = 0; h < S::kSteps; ++h) {
+            float one = 0.0f;                // ROWS: the row's scale
+            uint4 f[ROWS ? 1 : kPiece / 4];  // else: a piece's, one for each column
+            if constexpr (ROWS) one = lds_float(sc + h * M * 4);
 #pragma unroll
-        for (int i = 0; i < kPiece / 16; ++i) tmem_load16(at + 16 * i, v[0][i]);
+            for (int pc = 0; pc < kPieces; ++pc) {
+              if constexpr (!ROWS) {
 #pragma unroll
-        for (int pc = 0; pc < kPieces; ++pc) {
-          tmem_wait();
-          if (pc + 1 == kPieces) {  // the accumulator may be written again
-            tc_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(read);
-          } else {
+                for (int j = 0; j < kPiece / 4; ++j) f[j] = lds128(sc + 4 * pc * kPiece + 16 * j);
+              }
+              tmem_wait();
+              if constexpr (kPieces == 1) {
 #pragma unroll
-            for (int i = 0; i < kPiece / 16; ++i) tmem_load16(at + (pc + 1) * kPiece + 16 * i, v[(pc + 1) & 1][i]);
-          }
+                for (int l = 0; l < kLoads; ++l)
 #pragma unroll
-          for (int j = 0; j < kPiece; j += 4) {
-            const uint4 g = ROWS ? make_uint4(0, 0, 0, 0) : f[ROWS ? 0 : j / 4];
-            float* d = acc[h] + pc * kPiece + j;
-            const float* x = &v[pc & 1][j / 16][j % 16];
-            d[0] = fmaf(x[0], ROWS ? one : __uint_as_float(g.x), d[0]);
-            d[1] = fmaf(x[1], ROWS ? one : __uint_as_float(g.y), d[1]);
-            d[2] = fmaf(x[2], ROWS ? one : __uint_as_float(g.z), d[2]);
-            d[3] = fmaf(x[3], ROWS ? one : __uint_as_float(g.w), d[3]);
-          }
-          if constexpr (!ROWS) {
-            if (pc + 1 < kPieces) {
+                  for (int j = 0; j < 16; ++j) v[0][l][j] = v[1][l][j];
+              }
+              if (pc + 1 == kPieces) {
+                tc_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_acce + 8 * as);  // it may be written again
+                as = as + 1 == S::kAcc ? 0 : as + 1;
+                aph ^= as == 0;
+                if (h + 1 < S::kSteps || more) open();
+              } else {
 #pragma unroll
-              for (int j = 0; j < kPiece / 4; ++j) f[j] = lds128(sc + 4 * (pc + 1) * kPiece + 16 * j);
+                for (int l = 0; l < kLoads; ++l)
+                  tmem_load16(tm + as * S::kStepN + (pc + 1) * kPiece + 16 * l, v[(pc + 1) & 1][l]);
+              }
+#pragma unroll
+              for (int j = 0; j < kPiece; j += 4) {
+                const uint4 g = ROWS ? make_uint4(0, 0, 0, 0) : f[ROWS ? 0 : j / 4];
+                float* d = acc[h] + pc * kPiece + j;
+                const float* x = &v[pc & 1][j / 16][j % 16];
+                d[0] = fmaf(x[0], ROWS ? one : __uint_as_float(g.x), d[0]);
+                d[1] = fmaf(x[1], ROWS ? one : __uint_as_float(g.y), d[1]);
+                d[2] = fmaf(x[2], ROWS ? one : __uint_as_float(g.z), d[2]);
+                d[3] = fmaf(x[3], ROWS ? one : __uint_as_float(g.w), d[3]);
+              }
             }
           }
         }
-      }
-      if (++bi == bn) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(b_sce + 8 * (batch % S::kBatches));
+        if (lane == 0) mbar_arrive(b_sce + 8 * slot);
+        slot = slot + 1 == S::kBatches ? 0 : slot + 1;
+        sph ^= slot == 0;
       }
-      if (kb == nkb - 1 || n + 1 == mine) {
+      {
         const float poison = !fine || *bad ? __int_as_float(0x7fffffff) : 0.0f;
-        const bool whole = kb_first == 0 && kb == nkb - 1;
+        const bool whole = seg == nkb;
         float* part = reinterpret_cast<float*>(smem + S::part(first_tile ? 0 : 1));
 #pragma unroll
         for (int h = 0; h < S::kSteps; ++h) {
@@ -446,14 +481,24 @@ __global__ void __launch_bounds__(TcShape<ROWS, M, N>::kThreads, 1)
           for (int j = 0; j < S::kCols; ++j) acc[h][j] += poison;
           if (whole)
             store_tile<ROWS, S::kCols>(a, acc[h], (long long)w.tt * S::kTileRows + (ROWS ? row : c0),
-                                       w.ot * S::kTileCols + (ROWS ? c0 : row));
+                                       w.ot * S::kTileCols + (ROWS ? c0 : row),
+                                       reinterpret_cast<uint4*>(smem + S::kTurnAt + (ROWS ? (warp - 4) * kTurn : 0)));
           else if (S::kJoins) {
+            if constexpr (ROWS) {
 #pragma unroll
-            for (int j = 0; j < S::kCols; ++j) part[(c0 + j) * S::kPitch + row] = acc[h][j];
+              for (int j = 0; j < S::kCols; j += 4)
+                *reinterpret_cast<float4*>(part + row * S::kPitch + c0 + j) =
+                    make_float4(acc[h][j], acc[h][j + 1], acc[h][j + 2], acc[h][j + 3]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < S::kCols; ++j) part[(c0 + j) * S::kPitch + row] = acc[h][j];
+            }
           }
         }
         first_tile = false;
       }
+      n += seg;
+      w.kb += seg - 1;
       w.step(nkb, a.ots);
     }
   }
@@ -474,12 +519,20 @@ __global__ void __launch_bounds__(TcShape<ROWS, M, N>::kThreads, 1)
     const int tile = T0 + t, ot = tile % a.ots, tt = tile / a.ots;
     // neighbouring threads take neighbouring output columns
     const int live = (int)min((long long)S::kTileRows, a.rows - (long long)tt * S::kTileRows);
-    for (int e = rank * (int)blockDim.x + threadIdx.x; e < live * S::kTileCols; e += cl * (int)blockDim.x) {
-      const int r = e / S::kTileCols, o = e % S::kTileCols, col = ot * S::kTileCols + o;
-      const uint32_t at = (uint32_t)(ROWS ? o * S::kPitch + r : r * S::kPitch + o) * 4;
-      float s = 0.0f;
-      for (int b = i - 1; b <= last; ++b) s += remote_float(sbase + S::part(from[b].x == t ? 0 : 1) + at, b);
-      if (col < a.O) store_dt(a.out, a.odt, ((long long)tt * S::kTileRows + r) * a.ostride + col, s);
+    constexpr int Q = S::kTileCols / 4;
+    for (int e = rank * (int)blockDim.x + threadIdx.x; e < live * Q; e += cl * (int)blockDim.x) {
+      const int r = e / Q, o = e % Q * 4, col = ot * S::kTileCols + o;
+      const uint32_t at = (uint32_t)(r * S::kPitch + o) * 4;
+      float4 s = make_float4(0, 0, 0, 0);
+      for (int b = i - 1; b <= last; ++b) {
+        const float4 p = remote_float4(sbase + S::part(from[b].x == t ? 0 : 1) + at, b);
+        s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
+      }
+      const size_t to = ((long long)tt * S::kTileRows + r) * a.ostride + col;
+      if (col < a.O) store_dt(a.out, a.odt, to, s.x);
+      if (col + 1 < a.O) store_dt(a.out, a.odt, to + 1, s.y);
+      if (col + 2 < a.O) store_dt(a.out, a.odt, to + 2, s.z);
+      if (col + 3 < a.O) store_dt(a.out, a.odt, to + 3, s.w);
     }
   }
   cluster_sync();  // no block leaves while its parts are read

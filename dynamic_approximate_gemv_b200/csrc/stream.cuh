@@ -45,10 +45,13 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 // Bounded: false once the phase did not come.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity) {
   for (int i = 0; i < kMaxWaits; ++i)
     if (mbar_try(bar, parity)) return true;
   return false;
+}
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+  return mbar_try(bar, parity) || mbar_wait_long(bar, parity);
 }
 // A ready barrier takes 129 clocks to say so (B200, one warp), but several asked
 // together take no longer: whether all are in their phases.
@@ -85,10 +88,15 @@ __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
+// The warp's number and the block's rank in its cluster, through a shuffle, by
+// which the compiler knows that they are the same in every lane: branches on
+// them, and all that is computed from them, then need no convergence barriers
+// (a K block of the epilogue spent 500 of 750 clocks in those).
+__device__ __forceinline__ int warp_index() { return __shfl_sync(~0u, (int)(threadIdx.x >> 5), 0); }
+__device__ __forceinline__ int cluster_rank() {
+  int r;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
+  return __shfl_sync(~0u, r, 0);
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
@@ -99,6 +107,13 @@ __device__ __forceinline__ float remote_float(uint32_t addr, uint32_t rank) {
   float v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 remote_float4(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
   return v;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
