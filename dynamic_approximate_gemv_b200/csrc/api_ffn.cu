@@ -18,8 +18,7 @@ cudaError_t launch_turn_scales(const float* s, int mats, int nkb, int nsb, float
 cudaError_t launch_fp8_matmul(const TileMat& w, const float* ws, int I, int O, const uint8_t* x, int64_t xstride,
                               const float* xs, int64_t xsstride, int64_t rows, int odt, void* out, int64_t ostride,
                               cudaStream_t s);
-cudaError_t launch_moe(const MoeCall& c, cudaStream_t s);
-size_t moe_scratch_bytes(int n_tokens, int top_k, int F, int wk);
+cudaError_t launch_moe(const MoeCall& c, int sms, cudaStream_t s);
 }  // namespace effort
 
 using namespace effort;
@@ -34,7 +33,7 @@ struct effort_fp8_s {
 
 struct effort_moe_s {
   int dev = 0;
-  int E = 0, wk = 0, rdt = 0;
+  int sms = 0, E = 0, wk = 0, rdt = 0, rpitch = 0;
   int64_t I = 0, F = 0;
   DevBuf buf;  // cores of w1/w3, cores of w2, scales, router
   TileMat w13 = {}, w2 = {};
@@ -56,6 +55,10 @@ effort_status_t device_sms(int* sms) {
     return EFFORT_ERR_CUDA;
   }
   return EFFORT_OK;
+}
+
+size_t call_scratch(effort_moe_t h, MoeCall* c, char* base, int n_tokens, int top_k, int x_size) {
+  return moe_scratch(c, base, n_tokens, top_k, x_size, h->E, (int)h->I, (int)h->F, h->wk, h->w13.nkb, h->w2.nkb, h->sms);
 }
 
 effort_status_t launched(cudaError_t e) {
@@ -196,10 +199,14 @@ effort_status_t effort_moe_prepare(const effort_moe_weights_t* weights, void* st
   const int c13 = cdiv(2 * cdiv(F, 8), kGroupCores) * kGroupCores, c2 = cdiv(I, 8 * kGroupCores) * kGroupCores;
   const TileMat w13 = {nullptr, c13, cdiv(I, ke), (size_t)c13 * cdiv(I, ke) * kCoreBytes};
   const TileMat w2 = {nullptr, c2, cdiv(F, ke), (size_t)c2 * cdiv(F, ke) * kCoreBytes};
-  const size_t scale_n = (size_t)E * cdiv(I, kBlk) * cdiv(F, kBlk);
-  const size_t sbytes = q ? align_up(scale_n * 4, 256) : 0;
-  const size_t rbytes = a.router ? align_up((size_t)E * I * dtype_size(a.router_dtype), 256) : 0;
-  const size_t total = E * (w13.stride + w2.stride) + 3 * sbytes + rbytes + 256;
+  const int bi = cdiv(I, kBlk), bf = cdiv(F, kBlk);
+  const size_t scale_n = (size_t)E * bi * bf;
+  // the scales as [row block][K block], rows of whole 16 bytes
+  const size_t s13bytes = q ? align_up((size_t)E * bf * align4(bi) * 4, 256) : 0;
+  const size_t s2bytes = q ? align_up((size_t)E * bi * align4(bf) * 4, 256) : 0;
+  const int rpitch = (I + 7) / 8 * 8;  // the router's rows in whole 16 bytes
+  const size_t rsz = a.router ? dtype_size(a.router_dtype) : 0, rbytes = align_up((size_t)E * rpitch * rsz, 256);
+  const size_t total = E * (w13.stride + w2.stride) + 2 * s13bytes + s2bytes + rbytes + 256;
   if (!within_cap(total)) return EFFORT_ERR_NOMEM;
   effort_moe_s* h = new (std::nothrow) effort_moe_s();
   if (!h) return EFFORT_ERR_NOMEM;
@@ -209,14 +216,16 @@ effort_status_t effort_moe_prepare(const effort_moe_weights_t* weights, void* st
     delete h;
     return s;
   };
-  if (cudaGetDevice(&h->dev) != cudaSuccess) return fail(EFFORT_ERR_CUDA);
-  effort_status_t st = h->buf.alloc(total);
+  effort_status_t st = device_sms(&h->sms);
+  if (st != EFFORT_OK || cudaGetDevice(&h->dev) != cudaSuccess) return fail(EFFORT_ERR_CUDA);
+  st = h->buf.alloc(total);
   if (st != EFFORT_OK) return fail(st);
   h->E = E;
   h->I = I;
   h->F = F;
   h->wk = wk;
   h->rdt = (int)a.router_dtype;
+  h->rpitch = rpitch;
   char* b = (char*)h->buf.p;
   h->w13 = w13;
   h->w13.data = (const uint8_t*)b;
@@ -232,13 +241,14 @@ effort_status_t effort_moe_prepare(const effort_moe_weights_t* weights, void* st
   for (int i = 0; i < 3 && q; ++i) {
     *dst[i] = (const float*)b;
     if (e == cudaSuccess) e = launch_check_finite(src[i], scale_n, status, s);
-    if (e == cudaSuccess) e = cudaMemcpyAsync(b, src[i], scale_n * 4, cudaMemcpyDeviceToDevice, s);
-    b += sbytes;
+    if (e == cudaSuccess) e = launch_turn_scales(src[i], E, i < 2 ? bi : bf, i < 2 ? bf : bi, (float*)b, s);
+    b += i < 2 ? s13bytes : s2bytes;
   }
   if (a.router) {
     h->router = b;
+    if (e == cudaSuccess) e = cudaMemsetAsync(b, 0, rbytes, s);
     if (e == cudaSuccess)
-      e = cudaMemcpyAsync(b, a.router, (size_t)E * I * dtype_size(a.router_dtype), cudaMemcpyDeviceToDevice, s);
+      e = cudaMemcpy2DAsync(b, rpitch * rsz, a.router, I * rsz, I * rsz, E, cudaMemcpyDeviceToDevice, s);
   }
   if (e == cudaSuccess)
     e = launch_tile_weights(wk, a.w1, E, I, F, (uint8_t*)h->w13.data, w13.cores, w13.nkb, w13.stride, 1, status, s);
@@ -258,7 +268,7 @@ effort_status_t effort_moe_prepare(const effort_moe_weights_t* weights, void* st
 effort_status_t effort_moe_scratch_bytes(effort_moe_t h, int64_t n_tokens, int32_t top_k, size_t* bytes) {
   if (!h || !bytes || n_tokens < 0 || top_k < 1) return EFFORT_ERR_ARG;
   if (n_tokens > EFFORT_MAX_TOKENS || top_k > EFFORT_MAX_TOP_K) return EFFORT_ERR_UNSUPPORTED;
-  *bytes = moe_scratch_bytes((int)n_tokens, top_k, (int)h->F, h->wk);
+  *bytes = call_scratch(h, nullptr, nullptr, (int)n_tokens, top_k, 4);
   return EFFORT_OK;
 }
 
@@ -276,9 +286,11 @@ effort_status_t effort_moe_forward(effort_moe_t h, const void* x, effort_dtype_t
     return EFFORT_ERR_ARG;
   if (n_tokens > EFFORT_MAX_TOKENS || top_k > EFFORT_MAX_TOP_K) return EFFORT_ERR_UNSUPPORTED;
   if (n_tokens == 0) return EFFORT_OK;
-  if (scratch_bytes < moe_scratch_bytes((int)n_tokens, top_k, (int)h->F, h->wk)) return EFFORT_ERR_ARG;
-  DeviceGuard guard(h->dev);
   MoeCall c = {};
+  // the size asked for holds x in its widest type
+  if (scratch_bytes < call_scratch(h, nullptr, nullptr, (int)n_tokens, top_k, 4)) return EFFORT_ERR_ARG;
+  call_scratch(h, &c, (char*)scratch, (int)n_tokens, top_k, (int)dtype_size(x_dtype));
+  DeviceGuard guard(h->dev);
   c.w13 = h->w13;
   c.w2 = h->w2;
   c.s1 = h->s1;
@@ -288,6 +300,7 @@ effort_status_t effort_moe_forward(effort_moe_t h, const void* x, effort_dtype_t
   c.nsb2 = cdiv(h->I, kBlk);
   c.router = h->router;
   c.rdt = h->rdt;
+  c.rpitch = h->rpitch;
   c.wk = h->wk;
   c.n_experts = h->E;
   c.I = (int)h->I;
@@ -303,9 +316,7 @@ effort_status_t effort_moe_forward(effort_moe_t h, const void* x, effort_dtype_t
   c.out = out;
   c.odt = out_dtype;
   c.ostride = out_stride;
-  c.h = (float*)scratch;
-  c.hstride = (int64_t)h->w2.nkb * k_per_block(h->wk);
-  return launched(launch_moe(c, (cudaStream_t)stream));
+  return launched(launch_moe(c, h->sms, (cudaStream_t)stream));
 }
 
 effort_status_t effort_moe_get_info(effort_moe_t h, int32_t* n_experts, int64_t* in_dim, int64_t* hidden_dim,

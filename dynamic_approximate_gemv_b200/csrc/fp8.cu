@@ -98,10 +98,13 @@ struct FewRows {
   int odt, tiles, cluster, kw;
 };
 constexpr int kFewRowsMax = 16;
+constexpr int kFewExtra = 12 * 1024;  // the table of x's scales
+template <int NT>
+using FewShape = StreamShape<NT, 128, 16, kFewExtra>;
 
 template <int NT>
-__global__ void __launch_bounds__(StreamShape<NT, 128>::kThreads, 1) k_fp8_few_rows(const FewRows a) {
-  using S = StreamShape<NT, 128>;
+__global__ void __launch_bounds__(FewShape<NT>::kThreads, 1) k_fp8_few_rows(const FewRows a) {
+  using S = FewShape<NT>;
   constexpr int MT = S::kMT;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
@@ -261,8 +264,8 @@ template <int NT>
 static int few_rows_clusters(int cluster) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)cluster);
-  cfg.blockDim = dim3(StreamShape<NT, 128>::kThreads);
-  cfg.dynamicSmemBytes = StreamShape<NT, 128>::kSmem;
+  cfg.blockDim = dim3(FewShape<NT>::kThreads);
+  cfg.dynamicSmemBytes = FewShape<NT>::kSmem;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned)cluster;
@@ -286,7 +289,7 @@ static cudaError_t launch_few_rows(FewRows a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if (dev >= kMaxDevices) return cudaErrorInvalidDevice;
   if (fit[dev][0].load() == 0) {
-    e = cudaFuncSetAttribute(k_fp8_few_rows<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)StreamShape<NT, 128>::kSmem);
+    e = cudaFuncSetAttribute(k_fp8_few_rows<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FewShape<NT>::kSmem);
     if (e != cudaSuccess) return e;
     for (int i = 3; i >= 0; --i) fit[dev][i].store(few_rows_clusters<NT>(1 << i));
     if (fit[dev][0].load() < 1) return cudaErrorLaunchOutOfResources;
@@ -298,9 +301,9 @@ static cudaError_t launch_few_rows(FewRows a, cudaStream_t s) {
   for (int i = 0; i < 4; ++i) {
     const int cl = 1 << i, n = min(fit[dev][i].load(), a.tiles);
     if (n < 1 || cl > a.w.nkb) break;
-    if ((long long)cdiv(a.w.nkb, cl) * NT * 8 * 4 > StreamShape<NT, 128>::kExtra) continue;  // the table of x's scales
+    if ((long long)cdiv(a.w.nkb, cl) * NT * 8 * 4 > kFewExtra) continue;  // the table of x's scales
     const long long per = cdiv(a.tiles, n);
-    const long long cost = per * cdiv(a.w.nkb, cl) + (cl > 1 ? 24 * cdiv(per, StreamShape<NT, 128>::kMT) : 0);
+    const long long cost = per * cdiv(a.w.nkb, cl) + (cl > 1 ? 24 * cdiv(per, FewShape<NT>::kMT) : 0);
     if (ncl == 0 || cost * 102 < best * 100) {
       best = cost;
       a.cluster = cl;
@@ -308,13 +311,13 @@ static cudaError_t launch_few_rows(FewRows a, cudaStream_t s) {
     }
   }
   if (ncl == 0) return cudaErrorInvalidConfiguration;
-  a.kw = StreamShape<NT, 128>::kWarps;
+  a.kw = FewShape<NT>::kWarps;
   if (a.cluster == 1)
     while (a.kw > a.w.nkb) a.kw /= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(ncl * a.cluster));
-  cfg.blockDim = dim3(StreamShape<NT, 128>::kThreads);
-  cfg.dynamicSmemBytes = StreamShape<NT, 128>::kSmem;
+  cfg.blockDim = dim3(FewShape<NT>::kThreads);
+  cfg.dynamicSmemBytes = FewShape<NT>::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

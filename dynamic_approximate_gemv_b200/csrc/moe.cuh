@@ -6,10 +6,10 @@ namespace effort {
 
 struct MoeCall {
   TileMat w13, w2;              // cores of w1 and w3 in turn; w2
-  const float *s1, *s3, *s2;    // e4m3: scales [expert][K block][128 rows]
+  const float *s1, *s3, *s2;    // e4m3: scales [expert][row block][align4(K blocks)]
   int nsb13, nsb2;              // their row blocks
-  const void* router;
-  int rdt, wk, n_experts, I, F;
+  const void* router;           // [expert][rpitch], rows padded with zeros
+  int rdt, rpitch, wk, n_experts, I, F;
   const void* x;
   int xdt;
   long long xstride;
@@ -19,8 +19,15 @@ struct MoeCall {
   void* out;
   int odt;
   long long ostride;
-  float* h;                     // [pairs][hstride] hidden activations
-  long long hstride;
+  // scratch
+  void* xop;                    // [tokens][xpitch] x in its own type, in fragment order, padded with zeros
+  float* h;                     // [pairs][hpitch] hidden activations, likewise
+  float* z;                     // [K share][pairs][I] second products
+  int xpitch, hpitch, shares;   // shares: parts of the second product's K
 };
+
+// scratch of a call in bytes, carved into c where c is given (base: the caller's memory)
+size_t moe_scratch(MoeCall* c, char* base, int n_tokens, int top_k, int xdt_size, int n_experts, int I, int F, int wk,
+                   int nkb13, int nkb2, int sms);
 
 }  // namespace effort
