@@ -19,6 +19,8 @@ cudaError_t launch_fp8_matmul(const TileMat& w, const float* ws, int I, int O, c
                               const float* xs, int64_t xsstride, int64_t rows, int odt, void* out, int64_t ostride,
                               cudaStream_t s);
 cudaError_t launch_moe(const MoeCall& c, int sms, cudaStream_t s);
+cudaError_t launch_moe_bounds(const void* w1, const void* w3, const float* s1, const float* s3, int wk, int E, int I, int F,
+                              float2* bound, cudaStream_t s);
 }  // namespace effort
 
 using namespace effort;
@@ -38,6 +40,7 @@ struct effort_moe_s {
   DevBuf buf;  // cores of w1/w3, cores of w2, scales, router
   TileMat w13 = {}, w2 = {};
   const float *s1 = nullptr, *s3 = nullptr, *s2 = nullptr;
+  const float2* bound = nullptr;
   const void* router = nullptr;
 };
 
@@ -57,8 +60,8 @@ effort_status_t device_sms(int* sms) {
   return EFFORT_OK;
 }
 
-size_t call_scratch(effort_moe_t h, MoeCall* c, char* base, int n_tokens, int top_k, int x_size) {
-  return moe_scratch(c, base, n_tokens, top_k, x_size, h->E, (int)h->I, (int)h->F, h->wk, h->w13.nkb, h->w2.nkb, h->sms);
+size_t call_scratch(effort_moe_t h, MoeCall* c, char* base, int n_tokens, int top_k) {
+  return moe_scratch(c, base, n_tokens, top_k, h->E, (int)h->I, (int)h->F, h->wk, h->w13.nkb, h->w2.nkb, h->sms);
 }
 
 effort_status_t launched(cudaError_t e) {
@@ -206,7 +209,8 @@ effort_status_t effort_moe_prepare(const effort_moe_weights_t* weights, void* st
   const size_t s2bytes = q ? align_up((size_t)E * bi * align4(bf) * 4, 256) : 0;
   const int rpitch = (I + 7) / 8 * 8;  // the router's rows in whole 16 bytes
   const size_t rsz = a.router ? dtype_size(a.router_dtype) : 0, rbytes = align_up((size_t)E * rpitch * rsz, 256);
-  const size_t total = E * (w13.stride + w2.stride) + 2 * s13bytes + s2bytes + rbytes + 256;
+  const size_t nbytes = align_up((size_t)E * w2.nkb * sizeof(float2), 256);  // the column norms
+  const size_t total = E * (w13.stride + w2.stride) + 2 * s13bytes + s2bytes + rbytes + nbytes + 256;
   if (!within_cap(total)) return EFFORT_ERR_NOMEM;
   effort_moe_s* h = new (std::nothrow) effort_moe_s();
   if (!h) return EFFORT_ERR_NOMEM;
@@ -249,7 +253,10 @@ effort_status_t effort_moe_prepare(const effort_moe_weights_t* weights, void* st
     if (e == cudaSuccess) e = cudaMemsetAsync(b, 0, rbytes, s);
     if (e == cudaSuccess)
       e = cudaMemcpy2DAsync(b, rpitch * rsz, a.router, I * rsz, I * rsz, E, cudaMemcpyDeviceToDevice, s);
+    b += rbytes;
   }
+  h->bound = (const float2*)b;
+  if (e == cudaSuccess) e = launch_moe_bounds(a.w1, a.w3, a.s1, a.s3, wk, E, I, F, (float2*)b, s);
   if (e == cudaSuccess)
     e = launch_tile_weights(wk, a.w1, E, I, F, (uint8_t*)h->w13.data, w13.cores, w13.nkb, w13.stride, 1, status, s);
   if (e == cudaSuccess)
@@ -268,7 +275,7 @@ effort_status_t effort_moe_prepare(const effort_moe_weights_t* weights, void* st
 effort_status_t effort_moe_scratch_bytes(effort_moe_t h, int64_t n_tokens, int32_t top_k, size_t* bytes) {
   if (!h || !bytes || n_tokens < 0 || top_k < 1) return EFFORT_ERR_ARG;
   if (n_tokens > EFFORT_MAX_TOKENS || top_k > EFFORT_MAX_TOP_K) return EFFORT_ERR_UNSUPPORTED;
-  *bytes = call_scratch(h, nullptr, nullptr, (int)n_tokens, top_k, 4);
+  *bytes = call_scratch(h, nullptr, nullptr, (int)n_tokens, top_k);
   return EFFORT_OK;
 }
 
@@ -287,15 +294,15 @@ effort_status_t effort_moe_forward(effort_moe_t h, const void* x, effort_dtype_t
   if (n_tokens > EFFORT_MAX_TOKENS || top_k > EFFORT_MAX_TOP_K) return EFFORT_ERR_UNSUPPORTED;
   if (n_tokens == 0) return EFFORT_OK;
   MoeCall c = {};
-  // the size asked for holds x in its widest type
-  if (scratch_bytes < call_scratch(h, nullptr, nullptr, (int)n_tokens, top_k, 4)) return EFFORT_ERR_ARG;
-  call_scratch(h, &c, (char*)scratch, (int)n_tokens, top_k, (int)dtype_size(x_dtype));
+  if (scratch_bytes < call_scratch(h, nullptr, nullptr, (int)n_tokens, top_k)) return EFFORT_ERR_ARG;
+  call_scratch(h, &c, (char*)scratch, (int)n_tokens, top_k);
   DeviceGuard guard(h->dev);
   c.w13 = h->w13;
   c.w2 = h->w2;
   c.s1 = h->s1;
   c.s3 = h->s3;
   c.s2 = h->s2;
+  c.bound = h->bound;
   c.nsb13 = cdiv(h->F, kBlk);
   c.nsb2 = cdiv(h->I, kBlk);
   c.router = h->router;

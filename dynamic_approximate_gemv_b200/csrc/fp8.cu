@@ -100,7 +100,7 @@ struct FewRows {
 constexpr int kFewRowsMax = 16;
 constexpr int kFewExtra = 12 * 1024;  // the table of x's scales
 template <int NT>
-using FewShape = StreamShape<NT, 128, 16, kFewExtra>;
+using FewShape = StreamShape<NT * 8, 128, 16, kFewExtra>;
 
 template <int NT>
 __global__ void __launch_bounds__(FewShape<NT>::kThreads, 1) k_fp8_few_rows(const FewRows a) {

@@ -26,28 +26,82 @@ namespace effort {
 // ---------------------------------------------------------------- router
 constexpr int kRouterThreads = 512;
 
-// One block per token: x to fragment order, the logits by warps, the top-k by
-// one warp.
-template <typename T, int KE>
+// How x of type T (0 fp32, 1 binary16, 2 bfloat16) enters products with weights
+// of kind WK: exactly, or fp32 in 22 (24) bits.
+template <int WK, int T>
+struct XKind {
+  static constexpr bool kBF = WK == kWBF16;  // the matrix instruction's type
+  static constexpr bool kSame = T == (kBF ? kBF16 : kF16);
+  static constexpr bool kScaled = !kBF && !kSame;
+  static constexpr int kParts = kSame ? 1 : T == kF32 ? (kBF ? 3 : 2) : kBF ? 2 : 1;
+};
+// How the hidden activations enter the second product.  FEW: the result is
+// bfloat16, whose 8 bits 11 do not disturb; else 22 (binary16), 16 or 24 bits.
+template <int WK, int ODT>
+struct HKind {
+  static constexpr bool kBF = WK == kWBF16, kScaled = !kBF;
+  static constexpr int kParts = kBF ? (ODT == kF32 ? 3 : 2) : (ODT == kBF16 ? 1 : 2);
+};
+
+// One block per token: x in parts and its norm, the logits by warps, the top-k
+// by one warp.
+template <int WK, int T>
 __global__ void __launch_bounds__(kRouterThreads) k_moe_router(const MoeCall c) {
-  extern __shared__ float xs[];  // the token, fp32, padded with zeros to rpitch
-  __shared__ float logit[EFFORT_MAX_EXPERTS];
-  const int t = blockIdx.x, lane = threadIdx.x & 31, warp = warp_index(), E = c.n_experts;
+  using X = XKind<WK, T>;
+  constexpr int KE = WK == kWE4M3 ? 128 : 64, BLK = act_block<KE, X::kParts, X::kScaled>();
+  extern __shared__ float xs[];  // the token, fp32, padded with zeros to whole K blocks
+  __shared__ float logit[EFFORT_MAX_EXPERTS], wred[2][kRouterThreads / 32];
+  const int t = blockIdx.x, lane = threadIdx.x & 31, warp = warp_index(), E = c.n_experts, nkb = c.w13.nkb;
+  constexpr int W = kRouterThreads / 32;
   grid_dep_launch();
   grid_dep_wait();
-  const T* x = static_cast<const T*>(c.x) + t * c.xstride;
-  T* to = static_cast<T*>(c.xop) + (size_t)t * c.xpitch;
-  for (int k = threadIdx.x; k < c.xpitch; k += kRouterThreads) {
-    const T v = k < c.I ? x[k] : from_float<T>(0.0f);
-    to[k / KE * KE + frag_pos<T, KE>(k % KE)] = v;
-    if (k < c.rpitch) xs[k] = to_float(v);
+  float big = 0.0f;
+  for (int k = threadIdx.x; k < nkb * KE; k += kRouterThreads) {
+    const float v = k < c.I ? load_dt(c.x, T, t * c.xstride + k) : 0.0f;
+    xs[k] = v;
+    big = fmaxf(big, fabsf(v));
   }
-  // behind a hidden vector's end
-  for (int j = 0; j < c.top_k; ++j)
-    for (int k = c.F + threadIdx.x; k < c.hpitch; k += kRouterThreads)
-      c.h[(size_t)(t * c.top_k + j) * c.hpitch + k / KE * KE + frag_pos<float, KE>(k % KE)] = 0.0f;
-  if (c.gate_mode == EFFORT_GATE_GIVEN) return;
+#pragma unroll
+  for (int m = 16; m; m >>= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, m));
+  if (lane == 0) wred[0][warp] = big;
   __syncthreads();
+#pragma unroll
+  for (int w = 0; w < W; ++w) big = fmaxf(big, wred[0][w]);
+  // the norm, without overflow on the way
+  const float inv = big > 0.0f && big < INFINITY ? __fdiv_rn(1.0f, fmaxf(big, 1e-30f)) : 1.0f;
+  float sq = 0.0f;
+  char* to = c.xop + (size_t)t * c.xpitch;
+  for (int kb = warp; kb < nkb; kb += W) {
+    float up = 1.0f, down = 1.0f, m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < KE / 32; ++i) {
+      const float v = xs[kb * KE + 32 * i + lane];
+      m = fmaxf(m, fabsf(v));
+      sq += v * inv * (v * inv);
+    }
+    if constexpr (X::kScaled) {
+#pragma unroll
+      for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+      pow2_scale(m, &up, &down);
+      if (lane == 0) *reinterpret_cast<float*>(to + (size_t)kb * BLK + KE * 2 * X::kParts) = down;
+    }
+#pragma unroll
+    for (int i = 0; i < KE / 32; ++i) {
+      const int k = 32 * i + lane;
+      store_parts<X::kBF, X::kParts>(reinterpret_cast<uint16_t*>(to + (size_t)kb * BLK) + frag_pos<KE>(k), KE,
+                                     xs[kb * KE + k] * up);
+    }
+  }
+#pragma unroll
+  for (int m = 16; m; m >>= 1) sq += __shfl_xor_sync(~0u, sq, m);
+  if (lane == 0) wred[1][warp] = sq;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float q = 0.0f;
+    for (int w = 0; w < W; ++w) q += wred[1][w];
+    c.xnorm[t] = big < INFINITY ? big * sqrtf(q) : big;
+  }
+  if (c.gate_mode == EFFORT_GATE_GIVEN) return;
   for (int e = warp; e < E; e += kRouterThreads / 32) {
     float s = 0.0f;
     if (c.rdt == kF32) {
@@ -193,21 +247,39 @@ __device__ void make_plan(Plan* p, const int* ids, int pairs, int E, int cols, u
 }
 
 // ---------------------------------------------------------------- products
-template <int WK, typename T, int NT>
-using MoeShape = StreamShape<NT, (WK == kWE4M3 ? 128 : 64) * (int)sizeof(T), 64, (int)(sizeof(Plan) + 15) / 16 * 16>;
+constexpr int kPlanBytes = (int)(sizeof(Plan) + 15) / 16 * 16, kMoeExtra = kPlanBytes + EFFORT_MAX_TOKENS * 4;
+template <int WK, int PARTS, int ROWS>
+using MoeShape = StreamShape<ROWS, (WK == kWE4M3 ? 128 : 64) * 2 * PARTS, 64, kMoeExtra>;
 
-// DOWN: the second product (T is float).  FEW: see ActKind.
-template <int WK, typename T, bool FEW, int NT, bool DOWN>
-__global__ void __launch_bounds__(MoeShape<WK, T, NT>::kThreads, 1) k_moe_product(const MoeCall c) {
-  using S = MoeShape<WK, T, NT>;
-  using A = ActKind<WK, T, FEW>;
-  constexpr int MT = S::kMT, W = S::kWarps, KE = WK == kWE4M3 ? 128 : 64, KS = KE / 16, ROWB = KE * (int)sizeof(T);
+// The power of two that brings the hidden activations of one token and K block
+// into binary16's range before they are known: |silu(a) b| <= |a| |b|, each at
+// most the norm of x times the largest column norm of the block (with a factor
+// of 2 for the roundings).  Typical values lie 2^-9 to 2^-12 below that bound and
+// binary16 holds 29 binades below it in full, 11 (22) bits of each.
+__device__ __forceinline__ void hidden_scale(float xnorm, float2 n, float* up, float* down) {
+  const float a = xnorm * n.x, b = xnorm * n.y;
+  int e = (int)((__float_as_uint(a) >> 23) & 0xff) + (int)((__float_as_uint(b) >> 23) & 0xff) - 127 + 3;
+  e = max(30, min(e, 255 + 12));  // inf and NaN end up somewhere
+  // 2^(15 - (e - 127)), as pow2_scale does for its maximum's exponent
+  e = min(e, 253);
+  *up = __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23);
+  *down = __uint_as_float((uint32_t)(e - 14) << 23);
+}
+
+// PARTS, SCALED: of the activations read; HPARTS, HSCALED (first product): of
+// the hidden activations written.  ROWS: rows of a chunk.  DOWN: the second product.
+template <int WK, int PARTS, bool SCALED, int HPARTS, bool HSCALED, int ROWS, bool DOWN>
+__global__ void __launch_bounds__(MoeShape<WK, PARTS, ROWS>::kThreads, 1) k_moe_product(const MoeCall c) {
+  using S = MoeShape<WK, PARTS, ROWS>;
+  constexpr int NT = S::NT, MT = S::kMT, W = S::kWarps, KE = WK == kWE4M3 ? 128 : 64, KS = KE / 16;
+  constexpr int BLK = act_block<KE, PARTS, SCALED>(), HBLK = act_block<KE, HPARTS, HSCALED>();
   // every K block's sums apart, to be scaled, or all into one
-  constexpr bool kApart = WK == kWE4M3 || A::kScaled;
+  constexpr bool kApart = WK == kWE4M3 || SCALED;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   float* red = reinterpret_cast<float*>(smem + S::kRedAt);
   Plan* plan = reinterpret_cast<Plan*>(smem + S::kExtraAt);
+  float* xnorm = reinterpret_cast<float*>(smem + S::kExtraAt + kPlanBytes);
   const int lane = threadIdx.x & 31, warp = warp_index(), g = lane >> 2, q = lane & 3;
   const TileMat w = DOWN ? c.w2 : c.w13;
   const int nkb = w.nkb, nkb4 = align4(nkb), pairs = c.n_tokens * c.top_k;
@@ -215,8 +287,10 @@ __global__ void __launch_bounds__(MoeShape<WK, T, NT>::kThreads, 1) k_moe_produc
 
   grid_dep_launch();
   grid_dep_wait();
+  if (!DOWN && HSCALED)
+    for (int i = threadIdx.x; i < c.n_tokens; i += S::kThreads) xnorm[i] = c.xnorm[i];
   uint8_t* temp = smem + S::kRingAt;  // the ring is not in use yet
-  make_plan(plan, c.ids, pairs, c.n_experts, 8 * NT, reinterpret_cast<uint16_t*>(temp),
+  make_plan(plan, c.ids, pairs, c.n_experts, ROWS, reinterpret_cast<uint16_t*>(temp),
             reinterpret_cast<int*>(temp + 2 * kMaxPairs), warp, lane, S::kThreads);
   Ring<S> ring;
   ring.init(sbase, warp, lane);
@@ -257,15 +331,14 @@ __global__ void __launch_bounds__(MoeShape<WK, T, NT>::kThreads, 1) k_moe_produc
     const uint32_t buf = ring.next_buf(), bar = ring.next_bar();
     constexpr int kScales = WK == kWE4M3 ? (DOWN ? 1 : 2) : 0;
     if (lane == 0) {
-      mbar_expect(bar, P.n * 2 * kCoreBytes + P.count * ROWB + 16 * kScales);
+      mbar_expect(bar, P.n * 2 * kCoreBytes + P.count * BLK + 16 * kScales);
       bulk_load(buf, w.data + P.expert * w.stride + core_at(2 * P.t, pk, nkb), P.n * 2 * kCoreBytes, bar);
     }
     __syncwarp();
     if (lane >= 8 && lane - 8 < P.count) {
       const int p = plan->list[P.start + lane - 8];
-      const T* row = DOWN ? reinterpret_cast<const T*>(c.h) + (size_t)p * c.hpitch
-                          : static_cast<const T*>(c.xop) + (size_t)(p / c.top_k) * c.xpitch;
-      bulk_load(buf + S::kActAt + (lane - 8) * S::kRowPitch, row + pk * KE, ROWB, bar);
+      const char* row = DOWN ? c.h + (size_t)p * c.hpitch : c.xop + (size_t)(p / c.top_k) * c.xpitch;
+      bulk_load(buf + S::kActAt + (lane - 8) * S::kRowPitch, row + (size_t)pk * BLK, BLK, bar);
     }
     if (kScales > 0 && lane >= 1 && lane <= kScales) {
       const float* s = DOWN ? c.s2 : lane == 1 ? c.s1 : c.s3;
@@ -288,6 +361,8 @@ __global__ void __launch_bounds__(MoeShape<WK, T, NT>::kThreads, 1) k_moe_produc
     const Group G = group_at(u);
     u += G.n;
     const int live = NT == 1 ? 1 : (G.count + 7) / 8;
+    float2 bound = make_float2(0.0f, 0.0f);
+    if (!DOWN && HSCALED) bound = __ldg(c.bound + (size_t)G.expert * c.w2.nkb + G.t * 8 / KE);
     float acc[MT][NT][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -298,16 +373,16 @@ __global__ void __launch_bounds__(MoeShape<WK, T, NT>::kThreads, 1) k_moe_produc
     for (int kb = G.kb0 + warp; kb < G.kb1; kb += W) {
       uint32_t at;
       fine &= ring.wait(&at);
-      uint32_t b[A::kParts][NT][KS][2];
+      uint32_t b[PARTS][NT][KS][2];
       float sx[NT][2];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        float down = 1.0f;
-        if (j == 0 || j < live)
-          act_parts<WK, T, FEW, KS>(at + S::kActAt + (8 * j + g) * S::kRowPitch, q, 8 * j + g < G.count, &b[0][j], NT, &down);
-        // the lanes that hold column 2 q (+ 1) know its scale
+        act_load<PARTS, NT, KS>(at + S::kActAt + (8 * j + g) * S::kRowPitch, q, 8 * j + g < G.count, b, j);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) sx[j][e] = A::kScaled ? __shfl_sync(~0u, down, (2 * q + e) * 4) : 1.0f;
+        for (int e = 0; e < 2; ++e) {  // of the columns this lane has sums of
+          const int r = 8 * j + 2 * q + e;
+          sx[j][e] = SCALED && r < G.count ? lds_float(at + S::kActAt + r * S::kRowPitch + KE * 2 * PARTS) : 1.0f;
+        }
       }
       float sw[2] = {1.0f, 1.0f};  // of the tile's rows g and g + 8
       if constexpr (WK == kWE4M3) {
@@ -319,13 +394,13 @@ __global__ void __launch_bounds__(MoeShape<WK, T, NT>::kThreads, 1) k_moe_produc
         if (m >= G.n) break;
         if constexpr (kApart) {
           float d[NT][4] = {};
-          mma_tile<WK, NT, A::kParts, KS>(at + m * 2 * kCoreBytes, g, q, b, live, d);
+          mma_tile<WK, NT, PARTS, KS>(at + m * 2 * kCoreBytes, g, q, b, live, d);
 #pragma unroll
           for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[m][j][e] = fmaf(d[j][e] * sx[j][e & 1], sw[e >> 1], acc[m][j][e]);
         } else {
-          mma_tile<WK, NT, A::kParts, KS>(at + m * 2 * kCoreBytes, g, q, b, live, acc[m]);
+          mma_tile<WK, NT, PARTS, KS>(at + m * 2 * kCoreBytes, g, q, b, live, acc[m]);
         }
       }
       __syncwarp();  // every lane has read the stage
@@ -357,10 +432,21 @@ __global__ void __launch_bounds__(MoeShape<WK, T, NT>::kThreads, 1) k_moe_produc
       if constexpr (DOWN) {
         const int row = G.t * 16 + o;
         if (o < G.n * 16 && row < c.I) c.z[((size_t)G.share * pairs + p) * c.I + row] = a;
-      } else {
-        const int j = G.t * 8 + o;
-        if (o < G.n * 8 && j < c.F)
-          c.h[(size_t)p * c.hpitch + j / KE * KE + frag_pos<float, KE>(j % KE)] = __fdiv_rn(a, 1.0f + expf(-a)) * b;
+      } else if (o < G.n * 8) {
+        // behind the last hidden unit the weights are zero and so is the sum;
+        // the last K block is written to its end by its last tiles' threads
+        const int j = G.t * 8 + o, kb = j / KE;
+        char* blk = c.h + (size_t)p * c.hpitch + (size_t)kb * HBLK;
+        float up = 1.0f, down = 1.0f;
+        if (HSCALED) {
+          hidden_scale(xnorm[p / c.top_k], bound, &up, &down);
+          if (j % KE == 0) *reinterpret_cast<float*>(blk + KE * 2 * HPARTS) = down;
+        }
+        const float v = j < c.F ? __fdiv_rn(a, 1.0f + expf(-a)) * b : 0.0f;
+        store_parts<WK == kWBF16, HPARTS>(reinterpret_cast<uint16_t*>(blk) + frag_pos<KE>(j % KE), KE, v * up);
+        if (G.t + G.n == tiles && o / 8 == G.n - 1)  // the K block's rest
+          for (int k = j + 8; k < (kb + 1) * KE; k += 8)
+            store_parts<WK == kWBF16, HPARTS>(reinterpret_cast<uint16_t*>(blk) + frag_pos<KE>(k % KE), KE, 0.0f);
       }
     }
   }
@@ -381,6 +467,46 @@ __global__ void __launch_bounds__(256) k_moe_sum(const MoeCall c) {
     y += c.gates[p] * a;
   }
   store_dt(c.out, c.odt, t * c.ostride + i, y);
+}
+
+// ---------------------------------------------------------------- preparation
+__device__ __forceinline__ float weight_value(const void* w, int wk, size_t i) {
+  if (wk == kWE4M3) return e4m3_to_float(static_cast<const uint8_t*>(w)[i]);
+  return wk == kWF16 ? __half2float(static_cast<const __half*>(w)[i]) : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i]);
+}
+// The largest column norms of w1 (and w3: blockIdx.z = 1) over each K block of
+// hidden units.  One block of 256 threads per (K block, expert, matrix).
+__global__ void __launch_bounds__(256) k_moe_bounds(const void* w1, const void* w3, const float* s1, const float* s3, int wk,
+                                                    int I, int F, float2* bound) {
+  const int KE = k_per_block(wk), kb = blockIdx.x, e = blockIdx.y, parts = 256 / KE;
+  const void* w = blockIdx.z ? w3 : w1;
+  const float* s = blockIdx.z ? s3 : s1;
+  const int j = kb * KE + threadIdx.x % KE, part = threadIdx.x / KE;
+  __shared__ float sums[256];
+  float q = 0.0f;
+  if (j < F)
+    for (int i = part; i < I; i += parts) {
+      float v = weight_value(w, wk, ((size_t)e * I + i) * F + j);
+      if (wk == kWE4M3) v *= s[((size_t)e * cdiv(I, kBlk) + i / kBlk) * cdiv(F, kBlk) + j / kBlk];
+      q += v * v;
+    }
+  sums[threadIdx.x] = q;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float m = 0.0f;
+    for (int k = 0; k < KE; ++k) {
+      float t = 0.0f;
+      for (int p = 0; p < parts; ++p) t += sums[p * KE + k];
+      m = fmaxf(m, t);
+    }
+    float* b = reinterpret_cast<float*>(bound + (size_t)e * gridDim.x + kb);
+    b[blockIdx.z] = sqrtf(m);
+  }
+}
+cudaError_t launch_moe_bounds(const void* w1, const void* w3, const float* s1, const float* s3, int wk, int E, int I, int F,
+                              float2* bound, cudaStream_t s) {
+  k_moe_bounds<<<dim3((unsigned)cdiv(F, k_per_block(wk)), (unsigned)E, 2), 256, 0, s>>>(w1, w3, s1, s3, wk, I, F, bound);
+  return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------- host
@@ -412,49 +538,57 @@ static cudaError_t allow(K kernel, std::atomic<bool>* done, size_t smem) {
   return e;
 }
 
-template <int WK, typename T, bool FEW, int NT, bool DOWN>
+template <int WK, int PARTS, bool SCALED, int HPARTS, bool HSCALED, int ROWS, bool DOWN>
 static cudaError_t product(const MoeCall& c, int sms, cudaStream_t s) {
-  using S = MoeShape<WK, T, NT>;
+  using S = MoeShape<WK, PARTS, ROWS>;
   static_assert(S::kWarps * S::kStages * S::kStage >= 2 * kMaxPairs + 4 * EFFORT_MAX_EXPERTS, "the plan's working space");
   static std::atomic<bool> done[kMaxDevices];
-  cudaError_t e = allow(k_moe_product<WK, T, FEW, NT, DOWN>, done, S::kSmem);
+  const auto kernel = k_moe_product<WK, PARTS, SCALED, HPARTS, HSCALED, ROWS, DOWN>;
+  cudaError_t e = allow(kernel, done, S::kSmem);
   if (e != cudaSuccess) return e;
-  return start(k_moe_product<WK, T, FEW, NT, DOWN>, dim3((unsigned)sms), S::kThreads, S::kSmem, s, c);
+  return start(kernel, dim3((unsigned)sms), S::kThreads, S::kSmem, s, c);
 }
-template <int WK, typename T>
-static cudaError_t up(const MoeCall& c, int sms, cudaStream_t s) {
-  return c.n_tokens <= 8 ? product<WK, T, false, 1, false>(c, sms, s) : product<WK, T, false, 2, false>(c, sms, s);
+// Rows of a chunk: a chunk's rows are read beside every K block and kept in its
+// stage, so one token has room for more stages, and more than 16 rows would
+// take the ring's; the weights of a longer list are read again.
+template <int WK, int PARTS, bool SCALED, int HPARTS, bool HSCALED, bool DOWN>
+static cudaError_t by_rows(const MoeCall& c, int sms, cudaStream_t s) {
+  if (c.n_tokens == 1) return product<WK, PARTS, SCALED, HPARTS, HSCALED, 1, DOWN>(c, sms, s);
+  if (c.n_tokens <= 8) return product<WK, PARTS, SCALED, HPARTS, HSCALED, 8, DOWN>(c, sms, s);
+  return product<WK, PARTS, SCALED, HPARTS, HSCALED, 16, DOWN>(c, sms, s);
 }
-template <int WK, bool FEW>
-static cudaError_t down(const MoeCall& c, int sms, cudaStream_t s) {
-  return c.n_tokens <= 8 ? product<WK, float, FEW, 1, true>(c, sms, s) : product<WK, float, FEW, 2, true>(c, sms, s);
-}
-template <typename T, int KE>
-static cudaError_t router(const MoeCall& c, cudaStream_t s) {
-  static std::atomic<bool> done[kMaxDevices];
-  cudaError_t e = allow(k_moe_router<T, KE>, done, (EFFORT_MAX_IN_DIM + 8) * 4);
-  if (e != cudaSuccess) return e;
-  return start(k_moe_router<T, KE>, dim3((unsigned)c.n_tokens), kRouterThreads, (size_t)c.rpitch * 4, s, c);
-}
-template <int WK>
+template <int WK, int T, int ODT>
 static cudaError_t all(const MoeCall& c, int sms, cudaStream_t s) {
-  constexpr int KE = WK == kWE4M3 ? 128 : 64;
-  cudaError_t e = c.xdt == kF32 ? router<float, KE>(c, s) : c.xdt == kF16 ? router<__half, KE>(c, s) : router<__nv_bfloat16, KE>(c, s);
-  if (e == cudaSuccess)
-    e = c.xdt == kF32 ? up<WK, float>(c, sms, s) : c.xdt == kF16 ? up<WK, __half>(c, sms, s) : up<WK, __nv_bfloat16>(c, sms, s);
-  if (e == cudaSuccess) e = c.odt == kBF16 ? down<WK, true>(c, sms, s) : down<WK, false>(c, sms, s);
+  using X = XKind<WK, T>;
+  using H = HKind<WK, ODT>;
+  static std::atomic<bool> done[kMaxDevices];
+  const size_t smem = (size_t)c.w13.nkb * k_per_block(WK) * 4;
+  cudaError_t e = allow(k_moe_router<WK, T>, done, (EFFORT_MAX_IN_DIM + 128) * 4);
+  if (e == cudaSuccess) e = start(k_moe_router<WK, T>, dim3((unsigned)c.n_tokens), kRouterThreads, smem, s, c);
+  if (e == cudaSuccess) e = by_rows<WK, X::kParts, X::kScaled, H::kParts, H::kScaled, false>(c, sms, s);
+  if (e == cudaSuccess) e = by_rows<WK, H::kParts, H::kScaled, 1, false, true>(c, sms, s);
   if (e == cudaSuccess) e = start(k_moe_sum, dim3((unsigned)cdiv(c.I, 256), (unsigned)c.n_tokens), 256, 0, s, c);
   return e;
 }
-
-cudaError_t launch_moe(const MoeCall& c, int sms, cudaStream_t s) {
-  return c.wk == kWE4M3 ? all<kWE4M3>(c, sms, s) : c.wk == kWF16 ? all<kWF16>(c, sms, s) : all<kWBF16>(c, sms, s);
+template <int WK, int T>
+static cudaError_t by_out(const MoeCall& c, int sms, cudaStream_t s) {
+  return c.odt == kF32 ? all<WK, T, kF32>(c, sms, s) : c.odt == kF16 ? all<WK, T, kF16>(c, sms, s) : all<WK, T, kBF16>(c, sms, s);
+}
+template <int WK>
+static cudaError_t by_x(const MoeCall& c, int sms, cudaStream_t s) {
+  return c.xdt == kF32 ? by_out<WK, kF32>(c, sms, s) : c.xdt == kF16 ? by_out<WK, kF16>(c, sms, s) : by_out<WK, kBF16>(c, sms, s);
 }
 
-size_t moe_scratch(MoeCall* c, char* base, int n_tokens, int top_k, int xdt_size, int n_experts, int I, int F, int wk,
-                   int nkb13, int nkb2, int sms) {
+cudaError_t launch_moe(const MoeCall& c, int sms, cudaStream_t s) {
+  return c.wk == kWE4M3 ? by_x<kWE4M3>(c, sms, s) : c.wk == kWF16 ? by_x<kWF16>(c, sms, s) : by_x<kWBF16>(c, sms, s);
+}
+
+size_t moe_scratch(MoeCall* c, char* base, int n_tokens, int top_k, int n_experts, int I, int F, int wk, int nkb13,
+                   int nkb2, int sms) {
   const int ke = k_per_block(wk), pairs = n_tokens * top_k;
-  const int xpitch = nkb13 * ke, hpitch = nkb2 * ke;
+  // K blocks in their longest form
+  const int blk = wk == kWBF16 ? ke * 2 * 3 : ke * 2 * 2 + 16;
+  const int xpitch = nkb13 * blk, hpitch = nkb2 * blk;
   // K shares of the second product: the fewest that leave the SMs under 4% of
   // their time without a tile (by the experts that can be met), no share
   // shorter than one K block a warp
@@ -477,12 +611,14 @@ size_t moe_scratch(MoeCall* c, char* base, int n_tokens, int top_k, int xdt_size
     at += (bytes + 255) / 256 * 256;
     return o;
   };
-  const size_t x0 = take((size_t)n_tokens * xpitch * xdt_size);
-  const size_t h0 = take((size_t)pairs * hpitch * 4);
+  const size_t x0 = take((size_t)n_tokens * xpitch);
+  const size_t n0 = take((size_t)n_tokens * 4);
+  const size_t h0 = take((size_t)pairs * hpitch);
   const size_t z0 = take((size_t)shares * pairs * I * 4);
   if (c) {
     c->xop = base + x0;
-    c->h = (float*)(base + h0);
+    c->xnorm = (float*)(base + n0);
+    c->h = base + h0;
     c->z = (float*)(base + z0);
     c->xpitch = xpitch;
     c->hpitch = hpitch;

@@ -19,15 +19,17 @@ struct MoeCall {
   void* out;
   int odt;
   long long ostride;
+  const float2* bound;          // [expert][hidden K block] largest column norms of w1 and w3
   // scratch
-  void* xop;                    // [tokens][xpitch] x in its own type, in fragment order, padded with zeros
-  float* h;                     // [pairs][hpitch] hidden activations, likewise
+  char* xop;                    // [tokens] rows of activation blocks (stream.cuh)
+  float* xnorm;                 // [tokens] their norms
+  char* h;                      // [pairs] hidden activations, likewise
   float* z;                     // [K share][pairs][I] second products
-  int xpitch, hpitch, shares;   // shares: parts of the second product's K
+  int xpitch, hpitch, shares;   // bytes of a row; parts of the second product's K
 };
 
 // scratch of a call in bytes, carved into c where c is given (base: the caller's memory)
-size_t moe_scratch(MoeCall* c, char* base, int n_tokens, int top_k, int xdt_size, int n_experts, int I, int F, int wk,
-                   int nkb13, int nkb2, int sms);
+size_t moe_scratch(MoeCall* c, char* base, int n_tokens, int top_k, int n_experts, int I, int F, int wk, int nkb13,
+                   int nkb2, int sms);
 
 }  // namespace effort

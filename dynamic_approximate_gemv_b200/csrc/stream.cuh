@@ -22,8 +22,6 @@
 // long as both operands agree: lane q of a row's four takes 32 consecutive
 // bytes, which are two 16-byte reads that meet no bank twice.
 #pragma once
-#include <type_traits>
-
 #include "ffn_common.cuh"
 
 namespace effort {
@@ -174,15 +172,16 @@ __device__ __forceinline__ void pow2_scale(float amax, float* up, float* down) {
 
 // ---------------------------------------------------------------- shapes
 // What a stage holds and how many fit: W warps, MT tiles a group, ST stages a
-// warp.  ROWB: bytes of one K block of an activation row, PAD: bytes between
-// rows (with it no read of the fragments meets a bank twice), EXTRA: shared
-// memory of the caller's own.
+// warp.  ROWS: activation rows, ROWB: bytes of one K block of a row, PAD: bytes
+// between rows (with it no read of the fragments meets a bank twice), EXTRA:
+// shared memory of the caller's own.
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kStreamHead = 2048;    // barriers
-template <int NT, int ROWB, int PAD, int EXTRA>
+template <int ROWS, int ROWB, int PAD, int EXTRA>
 struct StreamShape {
+  static constexpr int NT = (ROWS + 7) / 8;  // column tiles of 8
   static constexpr int kRowPitch = ROWB + PAD;
-  static constexpr int kActBytes = NT * 8 * kRowPitch;
+  static constexpr int kActBytes = ROWS * kRowPitch;
   static constexpr int stage(int mt) { return mt * 2 * kCoreBytes + kActBytes + 64; }
   static constexpr int pitch(int mt) { return mt * 16 + 4; }  // floats of a column in the join, likewise
   static constexpr int red(int w, int mt) { return w * NT * 8 * pitch(mt) * 4; }
@@ -266,90 +265,53 @@ __device__ __forceinline__ void mma_tile(uint32_t tile, int g, int q, const uint
 }
 
 // ---------------------------------------------------------------- activations of 16 and 32 bits
-// Their rows lie in memory in the order of the fragments: of a K block of KE
-// elements lane q of a row's four multiplies KE / 4 neighbours, and the 16-byte
-// pieces of the four lanes alternate, so that a warp reads 64 bytes of a row.
-template <typename T, int KE>
+// Activations meet 16-bit operands in parts: v = p0 + p1 + .., each of 11
+// (binary16) or 8 (bfloat16) significant bits.  For binary16 a K block of a row
+// is first scaled by a power of two into its range, and the inverse stands
+// behind the parts.  The parts lie in the order of the fragments: of a K block
+// of KE elements lane q of a row's four multiplies KE / 4 neighbours, and the
+// 16-byte pieces of the four lanes alternate, so that a warp reads 64 bytes of
+// a row.
+template <int KE>
 __host__ __device__ __forceinline__ int frag_pos(int k) {
-  constexpr int L = KE / 4, V = 16 / (int)sizeof(T);
+  constexpr int L = KE / 4;
   const int q = k / L, r = k % L;
-  return (r / V * 4 + q) * V + r % V;
+  return (r / 8 * 4 + q) * 8 + r % 8;
 }
-
-// How x of type T enters products with weights of kind WK, in how many parts of
-// 11 (binary16) or 8 (bfloat16) bits, and whether each K block is first scaled
-// by a power of two into binary16's range.  FEW: the result is bfloat16, whose
-// 8 bits 11 do not disturb.
-template <int WK, typename T, bool FEW>
-struct ActKind {
-  static constexpr bool kBF = WK == kWBF16;  // the matrix instruction's type
-  static constexpr bool kF32 = sizeof(T) == 4, kSame = !kF32 && kBF == std::is_same_v<T, __nv_bfloat16>;
-  static constexpr bool kScaled = !kBF && !kSame;
-  static constexpr int kParts = kSame ? 1 : kF32 ? (kBF ? (FEW ? 2 : 3) : (FEW ? 1 : 2)) : kBF ? 2 : 1;
-};
-
-// B fragments of one column tile; down: what the sums are to be multiplied by.
-template <int WK, typename T, bool FEW, int KS>
-__device__ __forceinline__ void act_parts(uint32_t row, int q, bool there, uint32_t (*b)[KS][2], int part_stride,
-                                          float* down) {
-  using A = ActKind<WK, T, FEW>;
-  constexpr int KE = KS * 16, V = 16 / sizeof(T), C = KE / 4 / V;  // 16-byte pieces of a lane
-  uint4 raw[C];
+// bytes of one K block of a row
+template <int KE, int PARTS, bool SCALED>
+__host__ __device__ constexpr int act_block() {
+  return KE * 2 * PARTS + (SCALED ? 16 : 0);
+}
+// v (scaled) into the parts of one element
+template <bool BF16, int PARTS>
+__device__ __forceinline__ void store_parts(uint16_t* at, int stride, float v) {
 #pragma unroll
-  for (int i = 0; i < C; ++i) raw[i] = there ? lds128(row + (i * 4 + q) * 16) : make_uint4(0, 0, 0, 0);
-  *down = 1.0f;
-  if constexpr (A::kSame) {
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      b[0][s][0] = s % 2 ? raw[s / 2].z : raw[s / 2].x;
-      b[0][s][1] = s % 2 ? raw[s / 2].w : raw[s / 2].y;
+  for (int p = 0; p < PARTS; ++p) {
+    if constexpr (BF16) {
+      const __nv_bfloat16 h = __float2bfloat16_rn(v);
+      at[p * stride] = __bfloat16_as_ushort(h);
+      v -= __bfloat162float(h);
+    } else {
+      const __half h = __float2half_rn(v);
+      at[p * stride] = __half_as_ushort(h);
+      v -= __half2float(h);
     }
-    return;
-  } else {
-    float v[KE / 4];
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-      if constexpr (A::kF32) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[4 * i + j] = __uint_as_float(w[j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f = unpack2<std::is_same_v<T, __nv_bfloat16>>(w[j]);
-          v[8 * i + 2 * j] = f.x;
-          v[8 * i + 2 * j + 1] = f.y;
-        }
-      }
-    }
-    if constexpr (A::kScaled) {
-      float m = 0.0f;
-#pragma unroll
-      for (int k = 0; k < KE / 4; ++k) m = fmaxf(m, fabsf(v[k]));
-      m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
-      m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
-      float up;
-      pow2_scale(m, &up, down);
-#pragma unroll
-      for (int k = 0; k < KE / 4; ++k) v[k] *= up;
-    }
-#pragma unroll
-    for (int p = 0; p < A::kParts; ++p)
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float& x = v[4 * s + 2 * h];
-          float& y = v[4 * s + 2 * h + 1];
-          const uint32_t r = pack2<A::kBF>(x, y);
-          b[p * part_stride][s][h] = r;
-          if (p + 1 < A::kParts) {
-            const float2 f = unpack2<A::kBF>(r);
-            x -= f.x;
-            y -= f.y;
-          }
-        }
   }
+}
+// B fragments of one column tile; b: [part][NT][KS][2]
+template <int PARTS, int NT, int KS>
+__device__ __forceinline__ void act_load(uint32_t row, int q, bool there, uint32_t (&b)[PARTS][NT][KS][2], int j) {
+#pragma unroll
+  for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+    for (int i = 0; i < KS / 2; ++i) {
+      const uint4 v = there ? lds128(row + p * KS * 32 + (i * 4 + q) * 16) : make_uint4(0, 0, 0, 0);
+      b[p][j][2 * i][0] = v.x;
+      b[p][j][2 * i][1] = v.y;
+      b[p][j][2 * i + 1][0] = v.z;
+      b[p][j][2 * i + 1][1] = v.w;
+    }
 }
 
 // B fragments of one column tile from e4m3 rows in the stage: `left` bytes of
