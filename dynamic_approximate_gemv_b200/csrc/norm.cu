@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(W * 32) k_block_norm(const effort_block_norm_t
 // sum left the memory idle (68 against TIME us at 8192 x 4096).
 // KEEP: the weights are of type T.
 template <typename T, int W, int S, bool KEEP>
-__global__ void __launch_bounds__(W * 32, 16 / W) k_block_norm_rows(const effort_block_norm_t a) {
+__global__ void __launch_bounds__(W * 32, 24 / W) k_block_norm_rows(const effort_block_norm_t a) {
   using L = Lay<T, true>;
   constexpr int E = L::E;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -483,7 +483,7 @@ static cudaError_t go_rows_as(const effort_block_norm_t& a, int sms, cudaStream_
     if (e != cudaSuccess) return e;
     done[dev].store(true);
   }
-  const long long most = (long long)sms * (16 / W);
+  const long long most = (long long)sms * (24 / W);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.rows < most ? a.rows : most));
   cfg.blockDim = dim3(W * 32);
