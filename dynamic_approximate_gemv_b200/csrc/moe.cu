@@ -204,60 +204,50 @@ struct Plan {
 };
 static_assert(EFFORT_MAX_EXPERTS <= 256 && kMaxPairs <= 1 << 13, "a chunk's fields");
 
-// temp: 2 kMaxPairs + 4 EFFORT_MAX_EXPERTS bytes
-__device__ void make_plan(Plan* p, const int* ids, int pairs, int E, int cols, uint16_t* rank, int* cnt, int warp, int lane,
-                          int threads) {
+// place, id: kMaxPairs each; cnt: EFFORT_MAX_EXPERTS
+__device__ void make_plan(Plan* p, const int* ids, int pairs, int E, int cols, uint16_t* place, int16_t* id, int* cnt,
+                          int warp, int lane, int threads) {
   for (int e = threadIdx.x; e < E; e += threads) cnt[e] = 0;
+  for (int i = threadIdx.x; i < pairs; i += threads) {
+    const int v = ids[i];
+    id[i] = (int16_t)(v >= 0 && v < E ? v : -1);
+  }
   __syncthreads();
   if (warp == 0) {
     // a pair's place among those of its expert
     for (int b = 0; b < pairs; b += 32) {
-      const int id = b + lane < pairs ? ids[b + lane] : -1;
-      const bool ok = id >= 0 && id < E;
-      const unsigned same = __match_any_sync(~0u, ok ? id : -1 - lane);
-      const int before = __popc(same & ((1u << lane) - 1));
-      int base = 0;
-      if (ok) base = cnt[id];
+      const int e = b + lane < pairs ? id[b + lane] : -1;
+      const unsigned same = __match_any_sync(~0u, e >= 0 ? e : -1 - lane);
+      const int before = __popc(same & ((1u << lane) - 1)), base = e >= 0 ? cnt[e] : 0;
       __syncwarp();
-      if (ok) {
-        rank[b + lane] = (uint16_t)(base + before);
-        if (before == 0) cnt[id] = base + __popc(same);
+      if (e >= 0) {
+        place[b + lane] = (uint16_t)(base + before);
+        if (before == 0) cnt[e] = base + __popc(same);
       }
       __syncwarp();
     }
-    // starts of the lists and of the chunks, 8 experts a lane
-    constexpr int kPer = EFFORT_MAX_EXPERTS / 32;
-    int n = 0, m = 0;
+    // starts of the lists and of the chunks
+    int list0 = 0, chunk0 = 0;
+    for (int b = 0; b < E; b += 32) {
+      const int e = b + lane, k = e < E ? cnt[e] : 0, m = (k + cols - 1) / cols;
+      int n1 = k, m1 = m;  // sums up to and with this lane
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = lane * kPer + i, k = e < E ? cnt[e] : 0;
-      n += k;
-      m += (k + cols - 1) / cols;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(~0u, n1, d), y = __shfl_up_sync(~0u, m1, d);
+        if (lane >= d) n1 += x, m1 += y;
+      }
+      const int n0 = list0 + n1 - k, m0 = chunk0 + m1 - m;
+      for (int i = 0; i < m; ++i)
+        p->chunk[m0 + i] = (uint32_t)(n0 + i * cols) << 13 | (uint32_t)min(cols, k - i * cols) << 8 | (uint32_t)e;
+      if (e < E) cnt[e] = n0;
+      list0 += __shfl_sync(~0u, n1, 31);
+      chunk0 += __shfl_sync(~0u, m1, 31);
     }
-    int n0 = n, m0 = m;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int a = __shfl_up_sync(~0u, n0, d), b = __shfl_up_sync(~0u, m0, d);
-      if (lane >= d) n0 += a, m0 += b;
-    }
-    if (lane == 31) p->chunks = m0;
-    n0 -= n;
-    m0 -= m;
-    for (int i = 0; i < kPer; ++i) {
-      const int e = lane * kPer + i;
-      if (e >= E) break;
-      const int k = cnt[e];
-      for (int s = 0; s < k; s += cols)
-        p->chunk[m0++] = (uint32_t)(n0 + s) << 13 | (uint32_t)min(cols, k - s) << 8 | (uint32_t)e;
-      cnt[e] = n0;
-      n0 += k;
-    }
+    if (lane == 0) p->chunks = chunk0;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < pairs; i += threads) {
-    const int id = ids[i];
-    if (id >= 0 && id < E) p->list[cnt[id] + rank[i]] = (uint16_t)i;
-  }
+  for (int i = threadIdx.x; i < pairs; i += threads)
+    if (id[i] >= 0) p->list[cnt[id[i]] + place[i]] = (uint16_t)i;
   __syncthreads();
 }
 
@@ -306,43 +296,66 @@ __global__ void __launch_bounds__(MoeShape<WK, PARTS, ROWS>::kThreads, 1) k_moe_
     for (int i = threadIdx.x; i < c.n_tokens; i += S::kThreads) xnorm[i] = c.xnorm[i];
   uint8_t* temp = smem + S::kRingAt;  // the ring is not in use yet
   make_plan(plan, c.ids, pairs, c.n_experts, ROWS, reinterpret_cast<uint16_t*>(temp),
-            reinterpret_cast<int*>(temp + 2 * kMaxPairs), warp, lane, S::kThreads);
+            reinterpret_cast<int16_t*>(temp + 2 * kMaxPairs), reinterpret_cast<int*>(temp + 4 * kMaxPairs), warp, lane,
+            S::kThreads);
   Ring<S> ring;
   ring.init(sbase, warp, lane);
   const int units = plan->chunks * shares * tiles;
   const int u0 = (int)((long long)units * blockIdx.x / gridDim.x), u1 = (int)((long long)units * (blockIdx.x + 1) / gridDim.x);
 
-  // a group: up to MT tiles of one chunk (and K share), inside 64 stored rows
+  // A group: up to MT tiles of one chunk (and K share), inside 64 stored rows.
+  // kw warps share a group's K blocks; where those are few the block's warps
+  // form several sets, which take the groups in turn, so that a warp has three
+  // K blocks or more for each join.
+  int kw = W;
+  while (kw % 2 == 0 && nkb / shares < 3 * kw && (2 * W / kw) * MT <= u1 - u0) kw /= 2;
+  const int sets = W / kw, set = warp / kw, wk = warp % kw;
+  struct Cursor {
+    int u, seg, t, n;
+  };
+  auto size = [&](Cursor& c) { c.n = min(min(MT, 4 - (c.t & 3)), min(tiles - c.t, u1 - c.u)); };
+  auto next = [&](Cursor& c) {
+    c.u += c.n;
+    c.t += c.n;
+    if (c.t == tiles) c.t = 0, ++c.seg;
+    size(c);
+  };
+  Cursor first = {u0, u0 / tiles, u0 % tiles, 0};
+  size(first);
+  for (int i = 0; i < set && first.u < u1; ++i) next(first);
   struct Group {
     int expert, start, count, t, n, kb0, kb1, share;
   };
-  auto group_at = [&](int u) {
+  auto group_at = [&](const Cursor& cu) {
     Group G;
-    const int seg = u / tiles;
-    G.t = u - seg * tiles;
-    G.share = DOWN ? seg % shares : 0;
-    const uint32_t ch = plan->chunk[DOWN ? seg / shares : seg];
+    G.t = cu.t;
+    G.n = cu.n;
+    G.share = DOWN ? cu.seg % shares : 0;
+    const uint32_t ch = plan->chunk[DOWN ? cu.seg / shares : cu.seg];
     G.expert = ch & 255;
     G.count = ch >> 8 & 31;
     G.start = ch >> 13;
-    G.n = min(min(MT, 4 - (G.t & 3)), min(tiles - G.t, u1 - u));
     G.kb0 = DOWN ? nkb * G.share / shares : 0;
     G.kb1 = DOWN ? nkb * (G.share + 1) / shares : nkb;
     return G;
   };
+  auto step = [&](Cursor& cu) {
+    for (int i = 0; i < sets && cu.u < u1; ++i) next(cu);
+  };
   // what the warp asks for next
-  int pu = u0, pk = 0;
+  Cursor pc = first;
+  int pk = 0;
   Group P = {};
-  auto seek = [&]() {  // the first group from pu on that has a K block for this warp
-    while (pu < u1) {
-      P = group_at(pu);
-      pk = P.kb0 + warp;
+  auto seek = [&]() {  // the first group from pc on that has a K block for this warp
+    while (pc.u < u1) {
+      P = group_at(pc);
+      pk = P.kb0 + wk;
       if (pk < P.kb1) return;
-      pu += P.n;
+      step(pc);
     }
   };
   auto ask = [&]() {
-    if (pu >= u1) return;
+    if (pc.u >= u1) return;
     const uint32_t buf = ring.next_buf(), bar = ring.next_bar();
     constexpr int kScales = WK == kWE4M3 ? (DOWN ? 1 : 2) : 0;
     if (lane == 0) {
@@ -361,9 +374,9 @@ __global__ void __launch_bounds__(MoeShape<WK, PARTS, ROWS>::kThreads, 1) k_moe_
       bulk_load(buf + S::kScaleAt + 16 * (lane - 1), s + ((size_t)P.expert * nsb + blk) * nkb4 + (pk & ~3), 16, bar);
     }
     ++ring.put;
-    pk += W;
+    pk += kw;
     if (pk >= P.kb1) {
-      pu += P.n;
+      step(pc);
       seek();
     }
   };
@@ -372,9 +385,8 @@ __global__ void __launch_bounds__(MoeShape<WK, PARTS, ROWS>::kThreads, 1) k_moe_
   for (int s = 0; s < S::kStages; ++s) ask();
 
   bool fine = true;
-  for (int u = u0; u < u1;) {
-    const Group G = group_at(u);
-    u += G.n;
+  for (Cursor cu = first; cu.u < u1; step(cu)) {
+    const Group G = group_at(cu);
     const int live = NT == 1 ? 1 : (G.count + 7) / 8;
     float2 bound = make_float2(0.0f, 0.0f);
     if (!DOWN && HSCALED) bound = __ldg(c.bound + (size_t)G.expert * c.w2.nkb + G.t * 8 / KE);
@@ -385,7 +397,7 @@ __global__ void __launch_bounds__(MoeShape<WK, PARTS, ROWS>::kThreads, 1) k_moe_
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.0f;
-    for (int kb = G.kb0 + warp; kb < G.kb1; kb += W) {
+    for (int kb = G.kb0 + wk; kb < G.kb1; kb += kw) {
       uint32_t at;
       fine &= ring.wait(&at);
       uint32_t b[PARTS][NT][KS][2];
@@ -421,8 +433,8 @@ __global__ void __launch_bounds__(MoeShape<WK, PARTS, ROWS>::kThreads, 1) k_moe_
       __syncwarp();  // every lane has read the stage
       ask();
     }
-    // join the warps' sums
-    __syncthreads();
+    // join the set's sums
+    named_sync(set, kw * 32);
     float* mine = red + warp * S::kRed;
     const float poison = fine ? 0.0f : __int_as_float(0x7fffffff);
 #pragma unroll
@@ -432,16 +444,23 @@ __global__ void __launch_bounds__(MoeShape<WK, PARTS, ROWS>::kThreads, 1) k_moe_
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           mine[(8 * j + 2 * q + (e & 1)) * S::kPitch + 16 * m + g + 8 * (e >> 1)] = acc[m][j][e] + poison;
-    __syncthreads();
+    named_sync(set, kw * 32);
     constexpr int kWide = DOWN ? MT * 16 : MT * 8;  // outputs of a column
-    for (int i = threadIdx.x; i < G.count * kWide; i += S::kThreads) {
+    for (int i = wk * 32 + lane; i < G.count * kWide; i += kw * 32) {
       const int col = i / kWide, o = i % kWide;
-      const float* r = red + col * S::kPitch + (DOWN ? o : o / 8 * 16 + o % 8);
+      const float* r = red + set * kw * S::kRed + col * S::kPitch + (DOWN ? o : o / 8 * 16 + o % 8);
       float a = 0.0f, b = 0.0f;
+      if (kw == W) {
 #pragma unroll
-      for (int v = 0; v < W; ++v) {
-        a += r[v * S::kRed];
-        if (!DOWN) b += r[v * S::kRed + 8];
+        for (int v = 0; v < W; ++v) {
+          a += r[v * S::kRed];
+          if (!DOWN) b += r[v * S::kRed + 8];
+        }
+      } else {
+        for (int v = 0; v < kw; ++v) {
+          a += r[v * S::kRed];
+          if (!DOWN) b += r[v * S::kRed + 8];
+        }
       }
       const int p = plan->list[G.start + col];
       if constexpr (DOWN) {
@@ -556,7 +575,7 @@ static cudaError_t allow(K kernel, std::atomic<bool>* done, size_t smem) {
 template <int WK, int PARTS, bool SCALED, int HPARTS, bool HSCALED, int ROWS, bool DOWN>
 static cudaError_t product(const MoeCall& c, int sms, cudaStream_t s) {
   using S = MoeShape<WK, PARTS, ROWS>;
-  static_assert(S::kWarps * S::kStages * S::kStage >= 2 * kMaxPairs + 4 * EFFORT_MAX_EXPERTS, "the plan's working space");
+  static_assert(S::kWarps * S::kStages * S::kStage >= 4 * kMaxPairs + 4 * EFFORT_MAX_EXPERTS, "the plan's working space");
   static std::atomic<bool> done[kMaxDevices];
   const auto kernel = k_moe_product<WK, PARTS, SCALED, HPARTS, HSCALED, ROWS, DOWN>;
   cudaError_t e = allow(kernel, done, S::kSmem);
