@@ -128,11 +128,3 @@ def test_binding_refuses_host_tensors():
     with pytest.raises(ValueError):
         E.MoeLayer(torch.zeros(2, 8, 8).half(), torch.zeros(2, 8, 8).half(), torch.zeros(2, 8, 8).half())
 
-
-def test_the_norms_arguments_pack_as_their_structure():
-    from dynamic_approximate_gemv_b200 import ffn
-    assert ffn._NORM_PACK.size == ctypes.sizeof(ffn._NormArgs)
-    names = [n for n, _ in ffn._NormArgs._fields_]
-    values = [k + 1 for k in range(len(names))]
-    a = ffn._NormArgs.from_buffer_copy(ffn._NORM_PACK.pack(*values))
-    assert [getattr(a, n) for n in names] == values
