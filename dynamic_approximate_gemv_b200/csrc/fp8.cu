@@ -3,7 +3,6 @@
 //   out[r][n] = sum_b xs[r][b] ws[b][n / 128] sum_{k in b} x[r][k] w[k][n]
 //
 // and the layout of its weights.
-#include <stdlib.h>
 #include <atomic>
 
 #include "../../include/effort.h"
@@ -337,7 +336,14 @@ cudaError_t launch_fp8_tc(const TileMat& w, const float* ws, int I, int O, const
 cudaError_t launch_fp8_matmul(const TileMat& w, const float* ws, int I, int O, const uint8_t* x, int64_t xstride,
                               const float* xs, int64_t xsstride, int64_t rows, int odt, void* out, int64_t ostride,
                               cudaStream_t s) {
-  if (rows > (getenv("XTC") ? atoi(getenv("XTC")) : 16))
+  // Few rows stream through registers, with the least to set up: up to 8, and
+  // up to 16 of small matrices (16x1000x500: 2.9 against 4.1 us; 13x14336x4096:
+  // 24 against 15).  A wide and large matrix fills the tensor cores' tiles at
+  // once (8x4096x14336: 13.4 against 15.9 us; one row 13.2 against 13.8; but
+  // 8x14336x4096 15.2 against 13.5, 4x4096x4096 8.5 against 5.4).
+  const long long size = (long long)I * O;
+  const bool wide = rows > 1 && O >= 2 * I && size >= 32ll << 20;
+  if (wide || rows > kFewRowsMax || (rows > 8 && size > 2ll << 20))
     return launch_fp8_tc(w, ws, I, O, x, xstride, xs, xsstride, rows, odt, out, ostride, s);
   const size_t osz = odt == kF32 ? 4 : 2;
   // 16 rows' scales of a very long K do not fit beside the ring: 8 rows then

@@ -23,7 +23,6 @@
 // of its first and last tile.  Those parts are joined through distributed
 // shared memory once, at the end, in the blocks' order: no scratch, and the
 // same result every time.
-#include <stdlib.h>
 #include <atomic>
 #include <type_traits>
 
@@ -607,7 +606,7 @@ cudaError_t launch_fp8_tc(const TileMat& w, const float* ws, int I, int O, const
 #define GO(ROWS, M, N) return launch_tc<ROWS, M, N>(w, ws, I, O, x, xstride, xs, xsstride, rows, odt, out, ostride, s)
   if (rows <= 16) GO(false, 128, 16);
   if (rows <= 32) GO(false, 128, 32);
-  if (rows <= (getenv("XR") ? atoi(getenv("XR")) : 64)) GO(false, 128, 64);
+  if (rows <= 64) GO(false, 128, 64);
   if ((long long)cdiv(O, 256) * cdiv(rows, 128) < 100) GO(true, 128, 128);
   GO(true, 128, 256);
 #undef GO
