@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(FewShape<NT>::kThreads, 1) k_fp8_few_rows(cons
       }
     }
     // join the warps' sums (and the cluster's)
-    named_sync(wr, kw * 32);
+    set_sync(wr, kw);
     float* mine = red + warp * S::kRed;
     const float poison = fine ? 0.0f : __int_as_float(0x7fffffff);
 #pragma unroll
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(FewShape<NT>::kThreads, 1) k_fp8_few_rows(cons
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           mine[(8 * j + 2 * q + (e & 1)) * S::kPitch + 16 * m + g + 8 * (e >> 1)] = acc[m][j][e] + poison;
-    named_sync(wr, kw * 32);
+    set_sync(wr, kw);
     const int outs = n * 16 * a.rows;
     float* first = red + wr * kw * S::kRed;
     if (cl == 1) {

@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(MoeShape<WK, PARTS, ROWS>::kThreads, 1) k_moe_
       ask();
     }
     // join the set's sums
-    named_sync(set, kw * 32);
+    set_sync(set, kw);
     float* mine = red + warp * S::kRed;
     const float poison = fine ? 0.0f : __int_as_float(0x7fffffff);
 #pragma unroll
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(MoeShape<WK, PARTS, ROWS>::kThreads, 1) k_moe_
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           mine[(8 * j + 2 * q + (e & 1)) * S::kPitch + 16 * m + g + 8 * (e >> 1)] = acc[m][j][e] + poison;
-    named_sync(set, kw * 32);
+    set_sync(set, kw);
     constexpr int kWide = DOWN ? MT * 16 : MT * 8;  // outputs of a column
     for (int i = wk * 32 + lane; i < G.count * kWide; i += kw * 32) {
       const int col = i / kWide, o = i % kWide;

@@ -85,8 +85,12 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void named_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+// The barrier of one set of `warps` warps out of a block's; at most 8 sets of two
+// warps or more.  (Not barrier 0: that is the whole block's, and a set that has
+// gone on to the block's barrier must not meet another still at its own.)
+__device__ __forceinline__ void set_sync(int set, int warps) {
+  if (warps == 1) __syncwarp();
+  else asm volatile("bar.sync %0, %1;" ::"r"(set + 1), "r"(warps * 32) : "memory");
 }
 // The warp's number and the block's rank in its cluster, through a shuffle, by
 // which the compiler knows that they are the same in every lane: branches on
