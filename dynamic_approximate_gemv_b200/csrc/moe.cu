@@ -310,18 +310,47 @@ __global__ void __launch_bounds__(MoeShape<WK, PARTS, ROWS>::kThreads, 1) k_moe_
   int kw = W;
   while (kw % 2 == 0 && nkb / shares < 3 * kw && (2 * W / kw) * MT <= u1 - u0) kw /= 2;
   const int sets = W / kw, set = warp / kw, wk = warp % kw;
+  // The units' order: expert, K share, 64 stored rows, chunk of the expert, tile;
+  // so an expert of several chunks finds its weights in L2 for all but the first.
   struct Cursor {
-    int u, seg, t, n;
+    int u, c0, m, share, b, ch, t, n;  // c0, m: the expert's first chunk and their number; b: 64 rows
   };
-  auto size = [&](Cursor& c) { c.n = min(min(MT, 4 - (c.t & 3)), min(tiles - c.t, u1 - c.u)); };
+  const int chunks = plan->chunks;
+  auto same = [&](int c, int d) { return ((plan->chunk[c] ^ plan->chunk[d]) & 255) == 0; };
+  auto run = [&](int c0) {
+    int m = 1;
+    while (c0 + m < chunks && same(c0, c0 + m)) ++m;
+    return m;
+  };
+  auto size = [&](Cursor& c) { c.n = min(min(MT, min(4 * c.b + 4, tiles) - c.t), u1 - c.u); };
   auto next = [&](Cursor& c) {
     c.u += c.n;
     c.t += c.n;
-    if (c.t == tiles) c.t = 0, ++c.seg;
+    if (c.t == min(4 * c.b + 4, tiles)) {
+      if (++c.ch == c.m) {
+        c.ch = 0;
+        if (4 * ++c.b >= tiles) {
+          c.b = 0;
+          if (++c.share == shares) {
+            c.share = 0;
+            c.c0 += c.m;
+            if (c.c0 < chunks) c.m = run(c.c0);
+          }
+        }
+      }
+      c.t = 4 * c.b;
+    }
     size(c);
   };
-  Cursor first = {u0, u0 / tiles, u0 % tiles, 0};
-  size(first);
+  Cursor first = {u0, 0, 1, 0, 0, 0, 0, 0};
+  if (u0 < u1) {
+    int c0 = u0 / (shares * tiles);
+    while (c0 > 0 && same(c0 - 1, c0)) --c0;
+    const int m = run(c0), local = u0 - c0 * shares * tiles, share = local / (m * tiles), l = local - share * m * tiles;
+    const int b = l / (4 * m), nb = min(4, tiles - 4 * b), r = l - 4 * m * b;
+    first = {u0, c0, m, share, b, r / nb, 4 * b + r % nb, 0};
+    size(first);
+  }
   for (int i = 0; i < set && first.u < u1; ++i) next(first);
   struct Group {
     int expert, start, count, t, n, kb0, kb1, share;
@@ -330,8 +359,8 @@ __global__ void __launch_bounds__(MoeShape<WK, PARTS, ROWS>::kThreads, 1) k_moe_
     Group G;
     G.t = cu.t;
     G.n = cu.n;
-    G.share = DOWN ? cu.seg % shares : 0;
-    const uint32_t ch = plan->chunk[DOWN ? cu.seg / shares : cu.seg];
+    G.share = cu.share;
+    const uint32_t ch = plan->chunk[cu.c0 + cu.ch];
     G.expert = ch & 255;
     G.count = ch >> 8 & 31;
     G.start = ch >> 13;
