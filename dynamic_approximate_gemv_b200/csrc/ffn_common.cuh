@@ -4,11 +4,11 @@
 // Weight matrices are stored transposed ("rows" are output columns, K runs
 // along the input) and cut into cores of 8 rows x 128 bytes of K (128 e4m3
 // or 64 16-bit values), 1 KB each, in the order [matrix][row / 64][K block]
-// [row / 8 % 8].  A block that walks along K reads one contiguous stream, 8 KB
-// for each K block of 64 rows (with the K blocks of 8 rows together instead,
-// blocks in step met the same memory channels and a stream ended at a third
-// of the bandwidth), and one or two such groups are the operand tile of a
-// tensor-core product as they are.  Inside a core, the 16-byte
+// [row / 8 % 8].  A block that walks along K reads one contiguous stream, and a
+// K block of 64 rows (or of 16, 32 of them) is one copy; one or two such groups
+// are the operand tile of a tensor-core product as they are (a copy of 1 KB for
+// each core instead took the copying thread 1000 clocks a tile).  Inside a core,
+// the 16-byte
 // chunk c of row r lies at chunk c ^ r (the 128-byte swizzle): a warp's 16-byte
 // reads of eight rows meet no shared-memory bank twice, and the tensor core
 // takes the tile as it is.  Rows and K are padded with zeros.

@@ -295,7 +295,8 @@ __global__ void __launch_bounds__(W * 32) k_block_norm(const effort_block_norm_t
 // The same for many rows of whole runs: a block takes row after row, its inputs
 // two rows ahead in shared memory (bulk copies), and keeps the weights of its
 // columns in registers.  With direct loads a row's chain of load, sum, load,
-// sum left the memory idle (68 against TIME us at 8192 x 4096).
+// sum left the memory idle (68 against 53 us at 8192 x 4096 bf16, 106 against 71
+// with gate and e4m3).
 // KEEP: the weights are of type T.
 template <typename T, int W, int S, bool KEEP>
 __global__ void __launch_bounds__(W * 32, 24 / W) k_block_norm_rows(const effort_block_norm_t a) {
@@ -483,7 +484,9 @@ static cudaError_t go_rows_as(const effort_block_norm_t& a, int sms, cudaStream_
     if (e != cudaSuccess) return e;
     done[dev].store(true);
   }
-  const long long most = (long long)sms * (24 / W);
+  // blocks resident at once, by threads and by shared memory
+  const int by_smem = (int)(kSmemMax / (smem + 2048));
+  const long long most = (long long)sms * (24 / W < by_smem ? 24 / W : by_smem < 1 ? 1 : by_smem);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.rows < most ? a.rows : most));
   cfg.blockDim = dim3(W * 32);
