@@ -123,17 +123,17 @@ __device__ __forceinline__ void quantise(const effort_block_norm_t& a, long long
   // reciprocal, t = h y, and the remainder h - t s, which fused
   // multiply-add gives exactly, t + (h - t s) y is h / s rounded (Markstein's
   // theorem, 1990).  Where remainders could underflow, the division itself.
-  const float d = scale == 0.0f ? INFINITY : scale, y = __fdiv_rn(1.0f, d);
+  const float y = __fdiv_rn(1.0f, scale);
   float t[E];
   if (scale > 1e-25f && scale < 1e25f) {
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const float u = v[e] * y;
-      t[e] = fmaf(fmaf(-u, d, v[e]), y, u);
+      t[e] = fmaf(fmaf(-u, scale, v[e]), y, u);
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < E; ++e) t[e] = __fdiv_rn(v[e], d);
+    for (int e = 0; e < E; ++e) t[e] = scale == 0.0f ? 0.0f : __fdiv_rn(v[e], scale);
   }
   uint32_t b[E];
 #pragma unroll

@@ -371,7 +371,8 @@ effort_status_t effort_device_bytes_held(uint64_t* bytes);
  * stream as void*, argument errors found on the host before any launch), and
  * beyond them:
  *  - Strides are in elements, between rows; elements of a row are adjacent.
- *  - Sums, statistics and scales are held in fp32; each output is rounded once.
+ *  - Sums, statistics and scales are held in fp32; each output is rounded once
+ *    (what else is rounded is said below).
  *  - No call allocates, synchronises or keeps anything between calls: any of
  *    them may run on several streams at once, on one handle too, and may be
  *    captured into a graph.
@@ -403,8 +404,9 @@ typedef enum { EFFORT_NORM_NONE = 0, EFFORT_NORM_RMS = 1, EFFORT_NORM_LAYER = 2 
  *   h_out  h rounded to h_dtype.
  *   q_out, q_scales  h in e4m3 with a scale per row and EFFORT_BLOCK columns:
  *     scale = max |h| over the block / 448 (fp32), q = h / scale rounded to
- *     nearest even; a block of zeros (or one whose scale underflows to zero)
- *     has scale 0 and q 0.  A block that holds inf or NaN has scale inf or NaN.
+ *     nearest even (within +-448, which a subnormal scale's own rounding could
+ *     pass); a block of zeros (or one whose scale underflows to zero) has scale 0
+ *     and q 0.  A block that holds inf or NaN has scale inf or NaN.
  *     This is the form effort_fp8_matmul takes.
  * h is computed from x' before x' is rounded.
  *   dtype: of x, y, gate and x_out.  weight_dtype: of all weights and biases [dim].
@@ -463,7 +465,8 @@ effort_status_t effort_fp8_prepare(const void* q, const float* scales, int64_t i
  *   of 16 (what effort_block_norm writes for such a q_out); x_scales: device
  *   fp32 [rows x ceil(in_dim / 128)].  out: [rows x out_dim] of out_dtype.
  *   0 <= rows <= EFFORT_MAX_ROWS.  out overlaps neither input.
- *   One kernel; results do not vary from call to call.
+ *   One kernel (two for 9 to 16 rows where in_dim > 196608); results do not vary
+ *   from call to call.
  */
 effort_status_t effort_fp8_matmul(effort_fp8_t m, const void* x, int64_t x_stride, const float* x_scales,
                                   int64_t x_scales_stride, int64_t rows, effort_dtype_t out_dtype, void* out,
@@ -508,7 +511,8 @@ typedef struct {
 effort_status_t effort_moe_prepare(const effort_moe_weights_t* weights, void* stream, effort_moe_t* out_layer);
 
 /*
- * effort_moe_forward -- the layer on a few tokens:
+ * effort_moe_forward -- the layer on a few tokens (kernels: the router, the
+ *   first products, the second product, the weighted sum):
  *     out[t] = sum over j < top_k of gates[t][j] * expert_{ids[t][j]}(x[t]).
  *   gate_mode
  *     EFFORT_GATE_SOFTMAX_OF_TOP: logits l = router x[t]; ids = the top_k
@@ -527,6 +531,15 @@ effort_status_t effort_moe_prepare(const effort_moe_weights_t* weights, void* st
  *   bytes, 256-byte aligned, whose contents mean nothing before and after the
  *   call; calls that may overlap on the GPU bring scratch of their own.
  *   A token whose logits hold NaN counts them as lowest; its gates are NaN.
+ *   Precision: products of 16-bit and e4m3 values are exact.  x enters the
+ *   first products exactly where it is 16 bits wide, an fp32 x in 22 significant
+ *   bits (24 with bf16 weights).  The hidden activations silu(a) b enter the
+ *   second product in 11 bits where out is bf16, else in 22 (with bf16 weights:
+ *   16, and 24 where out is fp32); with binary16 and e4m3 weights those below
+ *   2^-26 of |x|^2 times the largest column norms of w1 and w3 (over 64 or 128
+ *   hidden units) keep fewer.  Results do not vary from call to call.
+ *   An expert's weights are read from memory once for up to 8 or 16 of its
+ *   tokens and again, mostly from L2, for each 8 or 16 more.
  */
 typedef enum {
   EFFORT_GATE_SOFTMAX_OF_TOP = 0,

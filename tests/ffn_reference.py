@@ -140,7 +140,10 @@ def moe(x, w1, w3, w2, ids, gates, out_dtype):
     """(out, error) in 64 bits; w1, w3, w2 in double [E, ...]; ids outside 0..E-1 add nothing."""
     e, i, f = w1.shape
     x64 = x.double()
-    # x itself enters in at least 22 bits, values below 2^-36 of a block's largest as nothing
+    # x itself enters in at least 22 bits, values below 2^-36 of a block's largest as nothing.
+    # The hidden activations are scaled by a power of two that brings B = |x|^2 |w1| |w3| (the
+    # largest column norms of a block; below: of the matrix) to 2^12 or more of binary16's
+    # 2^15, so half a step of its subnormals, 2^-25, is at most 2^-37 of B.
     dx = x64.abs() * 2.0 ** -21 + x64.abs().amax(1, keepdim=True) * 2.0 ** -36
     out = torch.zeros(x.shape[0], i, dtype=torch.float64, device=x.device)
     tol = torch.zeros_like(out)
@@ -160,7 +163,8 @@ def moe(x, w1, w3, w2, ids, gates, out_dtype):
         h = sg * b
         dsg = 1.1 * da + 8 * U32 * sg.abs()  # |silu'| < 1.1; exp, sum, quotient
         dh = dsg * (b.abs() + db) + sg.abs() * db + 4 * U32 * h.abs()
-        dh = dh + HIDDEN[out_dtype] * (h.abs() + dh) + h.abs().amax(1, keepdim=True) * 2.0 ** -36
+        bound = xt.square().sum(1, keepdim=True) * w1[j].norm(dim=0).max() * w3[j].norm(dim=0).max()
+        dh = dh + HIDDEN[out_dtype] * (h.abs() + dh) + bound * 2.0 ** -37
         g = gates[t, slot].double()[:, None]
         y = h @ w2[j]
         dy = dh @ w2[j].abs() + (h.abs() + dh) @ w2[j].abs() * steps(f)
