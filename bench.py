@@ -384,19 +384,21 @@ CHAIN_EQUALIZER = {"q": 0.5, "k": 0.5, "v": 0.5, "o": 0.5, "w1": 0.19, "w3": 0.1
 
 def chain_token(E, mats, x, effort):
     """One token through the stack: per layer x -> q, k, v; q -> o; o -> w1, w3;
-    w1 * w3 -> w2; every matvec input RMS-normalised (no gain).  `effort` is a
-    schedule (see effort_for)."""
+    w1 * w3 -> w2; every matvec input RMS-normalised (no gain) by the library's
+    norm, one kernel each (E None: the plain norm).  `effort` is a schedule (see
+    effort_for)."""
+    norm = rms_norm if E is None else (lambda v: E.block_norm(v).h)
     for l, L in enumerate(mats):
         e = {name: effort_for(effort, l, name) for name in L}
-        xn = rms_norm(x)
+        xn = norm(x)
         q = L["q"].gemv(xn, e["q"])
         L["k"].gemv(xn, e["k"])
         L["v"].gemv(xn, e["v"])
-        o = L["o"].gemv(rms_norm(q), e["o"])
-        h = rms_norm(o)
+        o = L["o"].gemv(norm(q), e["o"])
+        h = norm(o)
         a = L["w1"].gemv(h, e["w1"])
         b = L["w3"].gemv(h, e["w3"])
-        x = rms_norm(L["w2"].gemv(rms_norm(a * b), e["w2"]))
+        x = norm(L["w2"].gemv(norm(a * b), e["w2"]))
     return x
 
 
