@@ -60,13 +60,21 @@ template <typename T, bool RUN>
 struct Lay {
   static constexpr int E = RUN && sizeof(T) == 2 ? 8 : 4;
   static __device__ __forceinline__ int col(int base, int lane, int e) { return base + (RUN ? lane * E + e : e * 32 + lane); }
-  // a run is inside the row or outside of it, whole
-  static __device__ __forceinline__ void load(const T* row, int base, int lane, int n, float (&v)[E]) {
+  // U: float, or a type of 16 bits; a run is inside the row or outside of it, whole
+  template <typename U>
+  static __device__ __forceinline__ void load(const U* row, int base, int lane, int n, float (&v)[E]) {
     if constexpr (RUN) {
-      if (base + lane * E < n) load_run<T, E>(row + base + lane * E, v);
-      else {
+      const U* p = row + base + lane * E;
+      const bool in = base + lane * E < n;
+      if constexpr (E * sizeof(U) % 16 == 0) {
+        if (in) load_run<U, E>(p, v);
+        else {
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = 0.0f;
+          for (int e = 0; e < E; ++e) v[e] = 0.0f;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = in ? to_float(p[e]) : 0.0f;
       }
     } else {
 #pragma unroll
@@ -85,22 +93,9 @@ struct Lay {
   }
   // weights of a type known at run time
   static __device__ __forceinline__ void load_as(const void* row, int dt, int base, int lane, int n, float (&v)[E]) {
-    if constexpr (RUN) {
-      if (base + lane * E >= n) return;
-      const int c = base + lane * E;
-      if (dt == kF32) load_run<float, E>(static_cast<const float*>(row) + c, v);
-      else if constexpr (E == 8) {
-        if (dt == kF16) load_run<__half, E>(static_cast<const __half*>(row) + c, v);
-        else load_run<__nv_bfloat16, E>(static_cast<const __nv_bfloat16*>(row) + c, v);
-      } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = load_dt(row, dt, c + e);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (col(base, lane, e) < n) v[e] = load_dt(row, dt, col(base, lane, e));
-    }
+    if (dt == kF32) load(static_cast<const float*>(row), base, lane, n, v);
+    else if (dt == kF16) load(static_cast<const __half*>(row), base, lane, n, v);
+    else load(static_cast<const __nv_bfloat16*>(row), base, lane, n, v);
   }
 };
 
@@ -229,19 +224,36 @@ __global__ void __launch_bounds__(W * 32) k_block_norm(const effort_block_norm_t
 #pragma unroll
       for (int e = 0; e < E; ++e) t += v[s][e] * v[s][e];
     const float r = rsqrtf(sum(t) * inv_n + a.eps);
+    // the type is chosen once for all slots, so that their loads go out together
+    auto affine = [&](auto type) {
+      using U = decltype(type);
+      if (w) {
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      float f[E] = {};
-      if (w) L::load_as(w, a.weight_dtype, base(s), lane, n, f);
+        for (int s = 0; s < S; ++s) {
+          float f[E];
+          L::load(static_cast<const U*>(w), base(s), lane, n, f);
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[s][e] *= w ? r * (a.weight_offset + f[e]) : r;
-      if (b) {
-        float o[E] = {};
-        L::load_as(b, a.weight_dtype, base(s), lane, n, o);
+          for (int e = 0; e < E; ++e) v[s][e] *= r * (a.weight_offset + f[e]);
+        }
+      } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[s][e] += o[e];
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[s][e] *= r;
       }
-    }
+      if (b) {
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          float f[E];
+          L::load(static_cast<const U*>(b), base(s), lane, n, f);
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[s][e] += f[e];
+        }
+      }
+    };
+    if (a.weight_dtype == kF32) affine(0.0f);
+    else if (a.weight_dtype == kF16) affine(__half());
+    else affine(__nv_bfloat16());
   };
 
   grid_dep_launch();
@@ -254,15 +266,20 @@ __global__ void __launch_bounds__(W * 32) k_block_norm(const effort_block_norm_t
 #pragma unroll
       for (int s = 0; s < S; ++s) L::load(y, base(s), lane, n, v[s]);
       if (a.post_kind != EFFORT_NORM_NONE) norm(v, a.post_kind, a.post_weight, a.post_bias);
+      if (a.gate) {
+        const T* gate = static_cast<const T*>(a.gate) + r * a.gate_stride;
 #pragma unroll
-      for (int s = 0; s < S; ++s) {
-        float f[E], g[E];
-        L::load(x, base(s), lane, n, f);
-        if (a.gate) {
-          L::load(static_cast<const T*>(a.gate) + r * a.gate_stride, base(s), lane, n, g);
+        for (int s = 0; s < S; ++s) {
+          float g[E];
+          L::load(gate, base(s), lane, n, g);
 #pragma unroll
           for (int e = 0; e < E; ++e) v[s][e] *= g[e];
         }
+      }
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        float f[E];
+        L::load(x, base(s), lane, n, f);
 #pragma unroll
         for (int e = 0; e < E; ++e) v[s][e] = a.residual_scale * f[e] + a.branch_scale * v[s][e];
       }
@@ -549,8 +566,10 @@ static cudaError_t by_alignment(const effort_block_norm_t& a, int sms, cudaStrea
                    row(a.h_out, a.h_stride, hsz) && row(a.post_weight, 0, wsz) && row(a.post_bias, 0, wsz) &&
                    row(a.pre_weight, 0, wsz) && row(a.pre_bias, 0, wsz);
   if (!run) return by_dim<T, false>(a, sms, s);
-  // rows in turn pay from a few for each block on (one row: 3.7 us direct)
-  if (a.rows >= 4ll * sms && a.dim > 256) {
+  // rows in turn pay from a few for each block on (one row: 3.7 us direct); of
+  // rows that leave an SM one block only, from the second on (34 against 18 us
+  // at 308 x 13888 bf16 with gate and e4m3)
+  if (a.rows >= (a.dim > 8192 ? 1 : 4) * (long long)sms && a.dim > 256) {
     if (a.dim <= 1024) return go_rows<T, 2, 16>(a, sms, s);
     if (a.dim <= 2048) return go_rows<T, 4, 16>(a, sms, s);
     if (a.dim <= 4096) return go_rows<T, 8, 16>(a, sms, s);

@@ -35,6 +35,13 @@ def test_norm_many_rows(E, dim, dt):
     N.check(E, 777, dim, dt, "layer", "layer", "one", bias=True, off=1.0)
 
 
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("wdt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows,dim", [(200, 9000), (3, 12288), (5, 5003), (70, 8195)])
+def test_norm_long_rows_by_weight_type(E, rows, dim, wdt, dt):
+    N.check(E, rows, dim, dt, "rms", "layer", "row", bias=True, wdt=wdt, quantize=True)
+
+
 @pytest.mark.parametrize("wdt", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("form", [(None, "rms", None), ("rms", None, "one"), ("layer", "rms", None)])
@@ -92,6 +99,19 @@ def test_product_shapes(E, rows, i, o):
 @pytest.mark.parametrize("o", [1, 16, 17, 64, 127, 255, 256, 1001])
 def test_product_narrow(E, rows, o):
     P.check(E, rows, 1500, o, "bf16", o)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("rows,o", [(150, 75), (150, 300), (70, 511), (1000, 9000)])
+def test_product_writes_its_rows_only(E, rows, o, dt):
+    """Rows that start off 16 bytes, with what lies between them left as it was."""
+    wq, ws, q, s = P.operands(rows, 500, o)
+    m = E.Fp8Matrix(wq, ws)
+    ref = m.matmul(q, s, out_dtype=dt)
+    wide = torch.full((rows, o + 9), 7.0, device="cuda", dtype=dt)
+    m.matmul(q, s, out=wide[:, 3:3 + o])
+    assert torch.equal(wide[:, 3:3 + o], ref)
+    assert bool((wide[:, :3] == 7).all()) and bool((wide[:, 3 + o:] == 7).all())
 
 
 def test_product_scales_off_sixteen_bytes(E):
