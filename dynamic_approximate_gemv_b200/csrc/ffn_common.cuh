@@ -37,12 +37,6 @@ __host__ __device__ inline int cdiv(long long a, long long b) { return (int)((a 
 
 __host__ __device__ inline int align4(int x) { return (x + 3) & ~3; }
 
-// byte offset of element k (of esz bytes) of row r inside a core
-__device__ __forceinline__ int core_offset(int r, int k, int esz) {
-  const int b = k * esz;
-  return r * 128 + ((((b >> 4) ^ r) & 7) << 4) + (b & 15);
-}
-
 constexpr int kGroupCores = 8;       // cores that lie together
 constexpr int kGroupBytes = kGroupCores * kCoreBytes;
 // offset of a core in a matrix of nkb K blocks

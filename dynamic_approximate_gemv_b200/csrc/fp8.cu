@@ -164,9 +164,10 @@ __global__ void __launch_bounds__(FewShape<NT>::kThreads, 1) k_fp8_few_rows(cons
   }
   grid_dep_launch();
   grid_dep_wait();
+  // (plain loads: the kernel before may still have been writing when this one started)
   for (int i = threadIdx.x; i < (kb1 - kb0) * NT * 8; i += S::kThreads) {
     const int r = i / (kb1 - kb0), k = i % (kb1 - kb0);
-    const float s = r < a.rows ? __ldg(a.xs + r * a.xsstride + kb0 + k) : 0.0f;
+    const float s = r < a.rows ? a.xs[r * a.xsstride + kb0 + k] : 0.0f;
     *reinterpret_cast<float*>(smem + S::kExtraAt + (k * NT * 8 + r) * 4) = s;
   }
   ring.put = 0;

@@ -373,16 +373,17 @@ __global__ void __launch_bounds__(TcShape<ROWS, M, N>::kThreads, 1)
       for (int i = 0; i < R; ++i) {
         const long long r = (long long)at.tt * S::kTileRows + 32 * i + lane;
         const bool there = 32 * i + lane < S::kTileRows && r < a.rows;
+        // plain loads: the kernel before may still have been writing when this one started
         const float* p = a.xs + (there ? r : 0) * a.xsstride + kb;
         if (vec && (kb & 3) == 0 && n == S::kBatch) {
 #pragma unroll
           for (int k = 0; k < S::kBatch; k += 4) {
-            const float4 q = there ? __ldg(reinterpret_cast<const float4*>(p + k)) : make_float4(0, 0, 0, 0);
+            const float4 q = there ? *reinterpret_cast<const float4*>(p + k) : make_float4(0, 0, 0, 0);
             v[i][k] = q.x, v[i][k + 1] = q.y, v[i][k + 2] = q.z, v[i][k + 3] = q.w;
           }
         } else {
 #pragma unroll
-          for (int k = 0; k < S::kBatch; ++k) v[i][k] = there && k < n ? __ldg(p + k) : 0.0f;
+          for (int k = 0; k < S::kBatch; ++k) v[i][k] = there && k < n ? p[k] : 0.0f;
         }
       }
       if (batch >= S::kBatches) tc_wait(b_sce + 8 * sl, (batch / S::kBatches - 1) & 1, fine);

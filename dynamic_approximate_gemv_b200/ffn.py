@@ -87,7 +87,8 @@ def block_norm(x, y=None, *, post=None, post_weight=None, post_bias=None, gate=N
     Returns BlockNorm(x, h, q, scales): x' in x's dtype (x itself where nothing
     was added or scaled and no x_out is given), and h in out_dtype (default
     x's), or with quantize=True q (e4m3) and scales [rows, ceil(dim / 128)] in
-    its place, as Fp8Matrix.matmul takes them.  x_out and h_out may be x or y.
+    its place, as Fp8Matrix.matmul takes them.  x_out and h_out may be x or y
+    (with h_out=x and no x_out the returned x holds h).
     """
     if post not in _KIND or pre not in _KIND:
         raise ValueError("post and pre are 'rms', 'layer' or None")

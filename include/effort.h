@@ -462,7 +462,8 @@ effort_status_t effort_fp8_prepare(const void* q, const float* scales, int64_t i
  * effort_fp8_matmul -- out[r][n] = sum over blocks b of 128 of
  *     x_scales[r][b] * scales[b][n / 128] * sum over k in b of x[r][k] q[k][n].
  *   x: device e4m3 bytes [rows x in_dim], 16-byte aligned, x_stride a multiple
- *   of 16 (what effort_block_norm writes for such a q_out); x_scales: device
+ *   of 16 (what effort_block_norm writes for such a q_out), of which a row's
+ *   bytes are read up to the next multiple of 16 (any value); x_scales: device
  *   fp32 [rows x ceil(in_dim / 128)].  out: [rows x out_dim] of out_dtype.
  *   0 <= rows <= EFFORT_MAX_ROWS.  out overlaps neither input.
  *   One kernel (two for 9 to 16 rows where in_dim > 196608); results do not vary
