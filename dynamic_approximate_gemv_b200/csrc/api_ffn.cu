@@ -20,7 +20,7 @@ cudaError_t launch_fp8_matmul(const TileMat& w, const float* ws, int I, int O, c
                               cudaStream_t s);
 cudaError_t launch_moe(const MoeCall& c, int sms, cudaStream_t s);
 cudaError_t launch_moe_bounds(const void* w1, const void* w3, const float* s1, const float* s3, int wk, int E, int I, int F,
-                              float2* bound, cudaStream_t s);
+                              double2* bound, cudaStream_t s);
 }  // namespace effort
 
 using namespace effort;
@@ -40,7 +40,7 @@ struct effort_moe_s {
   DevBuf buf;  // cores of w1/w3, cores of w2, scales, router
   TileMat w13 = {}, w2 = {};
   const float *s1 = nullptr, *s3 = nullptr, *s2 = nullptr;
-  const float2* bound = nullptr;
+  const double2* bound = nullptr;
   const void* router = nullptr;
 };
 
@@ -209,7 +209,7 @@ effort_status_t effort_moe_prepare(const effort_moe_weights_t* weights, void* st
   const size_t s2bytes = q ? align_up((size_t)E * bi * align4(bf) * 4, 256) : 0;
   const int rpitch = (I + 7) / 8 * 8;  // the router's rows in whole 16 bytes
   const size_t rsz = a.router ? dtype_size(a.router_dtype) : 0, rbytes = align_up((size_t)E * rpitch * rsz, 256);
-  const size_t nbytes = align_up((size_t)E * w2.nkb * sizeof(float2), 256);  // the column norms
+  const size_t nbytes = align_up((size_t)E * w2.nkb * sizeof(double2), 256);  // the column norms
   const size_t total = E * (w13.stride + w2.stride) + 2 * s13bytes + s2bytes + rbytes + nbytes + 256;
   if (!within_cap(total)) return EFFORT_ERR_NOMEM;
   effort_moe_s* h = new (std::nothrow) effort_moe_s();
@@ -255,8 +255,8 @@ effort_status_t effort_moe_prepare(const effort_moe_weights_t* weights, void* st
       e = cudaMemcpy2DAsync(b, rpitch * rsz, a.router, I * rsz, I * rsz, E, cudaMemcpyDeviceToDevice, s);
     b += rbytes;
   }
-  h->bound = (const float2*)b;
-  if (e == cudaSuccess) e = launch_moe_bounds(a.w1, a.w3, a.s1, a.s3, wk, E, I, F, (float2*)b, s);
+  h->bound = (const double2*)b;
+  if (e == cudaSuccess) e = launch_moe_bounds(a.w1, a.w3, a.s1, a.s3, wk, E, I, F, (double2*)b, s);
   if (e == cudaSuccess)
     e = launch_tile_weights(wk, a.w1, E, I, F, (uint8_t*)h->w13.data, w13.cores, w13.nkb, w13.stride, 1, status, s);
   if (e == cudaSuccess)

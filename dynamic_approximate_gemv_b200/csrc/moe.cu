@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kRouterThreads) k_moe_router(const MoeCall c) 
   if (threadIdx.x == 0) {
     float q = 0.0f;
     for (int w = 0; w < W; ++w) q += wred[1][w];
-    c.xnorm[t] = big < INFINITY ? big * sqrtf(q) : big;
+    c.xnorm[t] = big < INFINITY ? (double)big * sqrt((double)q) : (double)big;
   }
   if (c.gate_mode == EFFORT_GATE_GIVEN) return;
   // a row of the router by one warp, or by several where there are few (their
@@ -252,23 +252,22 @@ __device__ void make_plan(Plan* p, const int* ids, int pairs, int E, int cols, u
 }
 
 // ---------------------------------------------------------------- products
-constexpr int kPlanBytes = (int)(sizeof(Plan) + 15) / 16 * 16, kMoeExtra = kPlanBytes + EFFORT_MAX_TOKENS * 4;
+constexpr int kPlanBytes = (int)(sizeof(Plan) + 15) / 16 * 16, kMoeExtra = kPlanBytes + EFFORT_MAX_TOKENS * 8;
 template <int WK, int PARTS, int ROWS>
 using MoeShape = StreamShape<ROWS, (WK == kWE4M3 ? 128 : 64) * 2 * PARTS, 64, kMoeExtra>;
 
 // The power of two that brings the hidden activations of one token and K block
 // into binary16's range before they are known: |silu(a) b| <= |a| |b|, each at
-// most the norm of x times the largest column norm of the block (with a factor
-// of 2 for the roundings).  Typical values lie 2^-9 to 2^-12 below that bound and
-// binary16 holds 29 binades below it in full, 11 (22) bits of each.
-__device__ __forceinline__ void hidden_scale(float xnorm, float2 n, float* up, float* down) {
-  const float a = xnorm * n.x, b = xnorm * n.y;
-  int e = (int)((__float_as_uint(a) >> 23) & 0xff) + (int)((__float_as_uint(b) >> 23) & 0xff) - 127 + 3;
-  e = max(30, min(e, 255 + 12));  // inf and NaN end up somewhere
-  // 2^(15 - (e - 127)), as pow2_scale does for its maximum's exponent
-  e = min(e, 253);
-  *up = __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23);
-  *down = __uint_as_float((uint32_t)(e - 14) << 23);
+// most the norm of x times the largest column norm of the block.  The bound is
+// held in 64 bits: one factor may lie far from 1 where the product does not.  It
+// comes to lie in [2^12, 2^13), a factor of 8 below binary16's largest value for the
+// roundings; typical values lie 2^-9 to 2^-12 below it.
+__device__ __forceinline__ void hidden_scale(double xnorm, double2 n, float* up, float* down) {
+  const double b = xnorm * n.x * (xnorm * n.y);
+  // b < 2^k; the values themselves are fp32 (inf and NaN end up somewhere)
+  const int k = max(-98, min((__double2hiint(b) >> 20 & 0x7ff) - 1022, 128));
+  *up = __uint_as_float((uint32_t)(127 + 13 - k) << 23);
+  *down = __uint_as_float((uint32_t)(127 - 13 + k) << 23);
 }
 
 // PARTS, SCALED: of the activations read; HPARTS, HSCALED (first product): of
@@ -284,7 +283,7 @@ __global__ void __launch_bounds__(MoeShape<WK, PARTS, ROWS>::kThreads, 1) k_moe_
   const uint32_t sbase = smem_u32(smem);
   float* red = reinterpret_cast<float*>(smem + S::kRedAt);
   Plan* plan = reinterpret_cast<Plan*>(smem + S::kExtraAt);
-  float* xnorm = reinterpret_cast<float*>(smem + S::kExtraAt + kPlanBytes);
+  double* xnorm = reinterpret_cast<double*>(smem + S::kExtraAt + kPlanBytes);
   const int lane = threadIdx.x & 31, warp = warp_index(), g = lane >> 2, q = lane & 3;
   const TileMat w = DOWN ? c.w2 : c.w13;
   const int nkb = w.nkb, nkb4 = align4(nkb), pairs = c.n_tokens * c.top_k;
@@ -417,7 +416,7 @@ __global__ void __launch_bounds__(MoeShape<WK, PARTS, ROWS>::kThreads, 1) k_moe_
   for (Cursor cu = first; cu.u < u1; step(cu)) {
     const Group G = group_at(cu);
     const int live = NT == 1 ? 1 : (G.count + 7) / 8;
-    float2 bound = make_float2(0.0f, 0.0f);
+    double2 bound = make_double2(0.0, 0.0);
     if (!DOWN && HSCALED) bound = __ldg(c.bound + (size_t)G.expert * c.w2.nkb + G.t * 8 / KE);
     float acc[MT][NT][4];
 #pragma unroll
@@ -430,20 +429,26 @@ __global__ void __launch_bounds__(MoeShape<WK, PARTS, ROWS>::kThreads, 1) k_moe_
       uint32_t at;
       fine &= ring.wait(&at);
       uint32_t b[PARTS][NT][KS][2];
-      float sx[NT][2];
+      float sc[NT][2][2];  // the scales of column 2 q + e and the tile's rows g, g + 8: x's is a power of two
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         act_load<PARTS, NT, KS>(at + S::kActAt + (8 * j + g) * S::kRowPitch, q, 8 * j + g < G.count, b, j);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {  // of the columns this lane has sums of
           const int r = 8 * j + 2 * q + e;
-          sx[j][e] = SCALED && r < G.count ? lds_float(at + S::kActAt + r * S::kRowPitch + KE * 2 * PARTS) : 1.0f;
+          sc[j][e][0] = sc[j][e][1] = SCALED && r < G.count ? lds_float(at + S::kActAt + r * S::kRowPitch + KE * 2 * PARTS) : 1.0f;
         }
       }
-      float sw[2] = {1.0f, 1.0f};  // of the tile's rows g and g + 8
       if constexpr (WK == kWE4M3) {
-        sw[0] = lds_float(at + S::kScaleAt + 4 * (kb & 3));
-        sw[1] = DOWN ? sw[0] : lds_float(at + S::kScaleAt + 16 + 4 * (kb & 3));
+        const float s0 = lds_float(at + S::kScaleAt + 4 * (kb & 3));
+        const float s1 = DOWN ? s0 : lds_float(at + S::kScaleAt + 16 + 4 * (kb & 3));
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            sc[j][e][0] *= s0;
+            sc[j][e][1] *= s1;
+          }
       }
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
@@ -454,7 +459,7 @@ __global__ void __launch_bounds__(MoeShape<WK, PARTS, ROWS>::kThreads, 1) k_moe_
 #pragma unroll
           for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[m][j][e] = fmaf(d[j][e] * sx[j][e & 1], sw[e >> 1], acc[m][j][e]);
+            for (int e = 0; e < 4; ++e) acc[m][j][e] = fmaf(d[j][e], sc[j][e & 1][e >> 1], acc[m][j][e]);
         } else {
           mma_tile<WK, NT, PARTS, KS>(at + m * 2 * kCoreBytes, g, q, b, live, acc[m]);
         }
@@ -538,36 +543,37 @@ __device__ __forceinline__ float weight_value(const void* w, int wk, size_t i) {
   return wk == kWF16 ? __half2float(static_cast<const __half*>(w)[i]) : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i]);
 }
 // The largest column norms of w1 (and w3: blockIdx.z = 1) over each K block of
-// hidden units.  One block of 256 threads per (K block, expert, matrix).
+// hidden units, in 64 bits, since squares of values and scales that fp32 holds may
+// leave its range.  One block of 256 threads per (K block, expert, matrix).
 __global__ void __launch_bounds__(256) k_moe_bounds(const void* w1, const void* w3, const float* s1, const float* s3, int wk,
-                                                    int I, int F, float2* bound) {
+                                                    int I, int F, double2* bound) {
   const int KE = k_per_block(wk), kb = blockIdx.x, e = blockIdx.y, parts = 256 / KE;
   const void* w = blockIdx.z ? w3 : w1;
   const float* s = blockIdx.z ? s3 : s1;
   const int j = kb * KE + threadIdx.x % KE, part = threadIdx.x / KE;
-  __shared__ float sums[256];
-  float q = 0.0f;
+  __shared__ double sums[256];
+  double q = 0.0;
   if (j < F)
     for (int i = part; i < I; i += parts) {
-      float v = weight_value(w, wk, ((size_t)e * I + i) * F + j);
+      double v = weight_value(w, wk, ((size_t)e * I + i) * F + j);
       if (wk == kWE4M3) v *= s[((size_t)e * cdiv(I, kBlk) + i / kBlk) * cdiv(F, kBlk) + j / kBlk];
       q += v * v;
     }
   sums[threadIdx.x] = q;
   __syncthreads();
   if (threadIdx.x == 0) {
-    float m = 0.0f;
+    double m = 0.0;
     for (int k = 0; k < KE; ++k) {
-      float t = 0.0f;
+      double t = 0.0;
       for (int p = 0; p < parts; ++p) t += sums[p * KE + k];
-      m = fmaxf(m, t);
+      m = fmax(m, t);
     }
-    float* b = reinterpret_cast<float*>(bound + (size_t)e * gridDim.x + kb);
-    b[blockIdx.z] = sqrtf(m);
+    double* b = reinterpret_cast<double*>(bound + (size_t)e * gridDim.x + kb);
+    b[blockIdx.z] = sqrt(m);
   }
 }
 cudaError_t launch_moe_bounds(const void* w1, const void* w3, const float* s1, const float* s3, int wk, int E, int I, int F,
-                              float2* bound, cudaStream_t s) {
+                              double2* bound, cudaStream_t s) {
   k_moe_bounds<<<dim3((unsigned)cdiv(F, k_per_block(wk)), (unsigned)E, 2), 256, 0, s>>>(w1, w3, s1, s3, wk, I, F, bound);
   return cudaGetLastError();
 }
@@ -677,12 +683,12 @@ size_t moe_scratch(MoeCall* c, char* base, int n_tokens, int top_k, int n_expert
     return o;
   };
   const size_t x0 = take((size_t)n_tokens * xpitch);
-  const size_t n0 = take((size_t)n_tokens * 4);
+  const size_t n0 = take((size_t)n_tokens * 8);
   const size_t h0 = take((size_t)pairs * hpitch);
   const size_t z0 = take((size_t)shares * pairs * I * 4);
   if (c) {
     c->xop = base + x0;
-    c->xnorm = (float*)(base + n0);
+    c->xnorm = (double*)(base + n0);
     c->h = base + h0;
     c->z = (float*)(base + z0);
     c->xpitch = xpitch;

@@ -19,10 +19,10 @@ struct MoeCall {
   void* out;
   int odt;
   long long ostride;
-  const float2* bound;          // [expert][hidden K block] largest column norms of w1 and w3
+  const double2* bound;         // [expert][hidden K block] largest column norms of w1 and w3
   // scratch
   char* xop;                    // [tokens] rows of activation blocks (stream.cuh)
-  float* xnorm;                 // [tokens] their norms
+  double* xnorm;                // [tokens] their norms
   char* h;                      // [pairs] hidden activations, likewise
   float* z;                     // [K share][pairs][I] second products
   int xpitch, hpitch, shares;   // bytes of a row; parts of the second product's K
