@@ -67,8 +67,8 @@ __global__ void __launch_bounds__(kRouterThreads) k_moe_router(const MoeCall c) 
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < W; ++w) big = fmaxf(big, wred[0][w]);
-  // the norm, without overflow on the way
-  const float inv = big > 0.0f && big < INFINITY ? __fdiv_rn(1.0f, fmaxf(big, 1e-30f)) : 1.0f;
+  // the norm, of quotients by the largest value (or 1e-30), so that no square leaves the range
+  const float unit = fmaxf(big, 1e-30f), inv = big < INFINITY ? __fdiv_rn(1.0f, unit) : 1.0f;
   float sq = 0.0f;
   char* to = c.xop + (size_t)t * c.xpitch;
   for (int kb = warp; kb < nkb; kb += W) {
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kRouterThreads) k_moe_router(const MoeCall c) 
   if (threadIdx.x == 0) {
     float q = 0.0f;
     for (int w = 0; w < W; ++w) q += wred[1][w];
-    c.xnorm[t] = big < INFINITY ? (double)big * sqrt((double)q) : (double)big;
+    c.xnorm[t] = big < INFINITY ? (double)unit * sqrt((double)q) : (double)big;
   }
   if (c.gate_mode == EFFORT_GATE_GIVEN) return;
   // a row of the router by one warp, or by several where there are few (their

@@ -37,6 +37,12 @@ def check(E, x, std1, std3, std2, i=256, f=192, e=2):
     layer.close()
 
 
+@pytest.mark.parametrize("mag", [1e-29, 1e-31, 1e-32, 1e-33])
+def test_tiny_x_under_large_scales(E, mag):
+    """The hidden activations' scale comes from the norm of x, however small x is."""
+    check(E, mag * randn(9, 3, 256), 1e-12 / mag, 1e-12 / mag, 1e10)
+
+
 @pytest.mark.parametrize("std1,std3,std2", [(1e-24, 1e14, 1e9), (1e14, 1e-24, 1e9), (1e20, 1e-10, 1e-10),
                                             (1e-10, 1e20, 1e-10), (1e-25, 1e25, 1.0), (1e25, 1e-25, 1.0)])
 def test_opposite_scales(E, std1, std3, std2):
