@@ -20,7 +20,7 @@ cudaError_t launch_fp8_matmul(const TileMat& w, const float* ws, int I, int O, c
                               cudaStream_t s);
 cudaError_t launch_moe(const MoeCall& c, int sms, cudaStream_t s);
 cudaError_t launch_moe_bounds(const void* w1, const void* w3, const float* s1, const float* s3, int wk, int E, int I, int F,
-                              double2* bound, cudaStream_t s);
+                              double2* bound, unsigned* status, cudaStream_t s);
 }  // namespace effort
 
 using namespace effort;
@@ -41,6 +41,7 @@ struct effort_moe_s {
   TileMat w13 = {}, w2 = {};
   const float *s1 = nullptr, *s3 = nullptr, *s2 = nullptr;
   const double2* bound = nullptr;
+  bool spread = false;
   const void* router = nullptr;
 };
 
@@ -256,7 +257,7 @@ effort_status_t effort_moe_prepare(const effort_moe_weights_t* weights, void* st
     b += rbytes;
   }
   h->bound = (const double2*)b;
-  if (e == cudaSuccess) e = launch_moe_bounds(a.w1, a.w3, a.s1, a.s3, wk, E, I, F, (double2*)b, s);
+  if (e == cudaSuccess) e = launch_moe_bounds(a.w1, a.w3, a.s1, a.s3, wk, E, I, F, (double2*)b, status, s);
   if (e == cudaSuccess)
     e = launch_tile_weights(wk, a.w1, E, I, F, (uint8_t*)h->w13.data, w13.cores, w13.nkb, w13.stride, 1, status, s);
   if (e == cudaSuccess)
@@ -267,7 +268,8 @@ effort_status_t effort_moe_prepare(const effort_moe_weights_t* weights, void* st
   if (e == cudaSuccess) e = cudaMemcpyAsync(&bad, status, 4, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return fail(EFFORT_ERR_CUDA);
-  if (bad) return fail(EFFORT_ERR_NONFINITE);
+  if (bad & 1) return fail(EFFORT_ERR_NONFINITE);
+  h->spread = (bad & 2) != 0;
   *out_layer = h;
   return EFFORT_OK;
 }
@@ -303,6 +305,7 @@ effort_status_t effort_moe_forward(effort_moe_t h, const void* x, effort_dtype_t
   c.s3 = h->s3;
   c.s2 = h->s2;
   c.bound = h->bound;
+  c.spread = h->spread;
   c.nsb13 = cdiv(h->F, kBlk);
   c.nsb2 = cdiv(h->I, kBlk);
   c.router = h->router;

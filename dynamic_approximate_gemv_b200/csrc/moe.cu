@@ -35,8 +35,11 @@ struct XKind {
   static constexpr bool kScaled = !kBF && !kSame;
   static constexpr int kParts = kSame ? 1 : T == kF32 ? (kBF ? 3 : 2) : kBF ? 2 : 1;
 };
-// How the hidden activations enter the second product.  FEW: the result is
-// bfloat16, whose 8 bits 11 do not disturb; else 22 (binary16), 16 or 24 bits.
+// How the hidden activations enter the second product: with bfloat16 weights in
+// 16 or (out fp32) 24 bits, else in 22, or in 11 for a bfloat16 out, whose 8 bits
+// they do not disturb: 261 against 297 us at 16 tokens of 8 x 4096 x 14336, top 2,
+// e4m3, 80 against 84 at one.  (Layers whose columns differ much take 22 there too:
+// see all().)
 template <int WK, int ODT>
 struct HKind {
   static constexpr bool kBF = WK == kWBF16, kScaled = !kBF;
@@ -260,14 +263,15 @@ using MoeShape = StreamShape<ROWS, (WK == kWE4M3 ? 128 : 64) * 2 * PARTS, 64, kM
 // into binary16's range before they are known: |silu(a) b| <= |a| |b|, each at
 // most the norm of x times the largest column norm of the block.  The bound is
 // held in 64 bits: one factor may lie far from 1 where the product does not.  It
-// comes to lie in [2^12, 2^13), a factor of 8 below binary16's largest value for the
-// roundings; typical values lie 2^-9 to 2^-12 below it.
+// comes to lie in [2^14, 2^15), half of binary16's largest value or less, which
+// leaves room for the roundings; typical values lie 2^9 to 2^12 below it, and
+// lower by as much as some column of the block, or some input, stands out.
 __device__ __forceinline__ void hidden_scale(double xnorm, double2 n, float* up, float* down) {
   const double b = xnorm * n.x * (xnorm * n.y);
   // b < 2^k; the values themselves are fp32 (inf and NaN end up somewhere)
-  const int k = max(-98, min((__double2hiint(b) >> 20 & 0x7ff) - 1022, 128));
-  *up = __uint_as_float((uint32_t)(127 + 13 - k) << 23);
-  *down = __uint_as_float((uint32_t)(127 - 13 + k) << 23);
+  const int k = max(-111, min((__double2hiint(b) >> 20 & 0x7ff) - 1022, 128));
+  *up = __uint_as_float((uint32_t)(127 + 15 - k) << 23);
+  *down = __uint_as_float((uint32_t)(127 - 15 + k) << 23);
 }
 
 // PARTS, SCALED: of the activations read; HPARTS, HSCALED (first product): of
@@ -544,9 +548,11 @@ __device__ __forceinline__ float weight_value(const void* w, int wk, size_t i) {
 }
 // The largest column norms of w1 (and w3: blockIdx.z = 1) over each K block of
 // hidden units, in 64 bits, since squares of values and scales that fp32 holds may
-// leave its range.  One block of 256 threads per (K block, expert, matrix).
+// leave its range.  One block of 256 threads per (K block, expert, matrix).  Bit 1
+// of status is set where norms of one K block (but zero) differ by more than kSpread.
+constexpr double kSpread = 32.0;
 __global__ void __launch_bounds__(256) k_moe_bounds(const void* w1, const void* w3, const float* s1, const float* s3, int wk,
-                                                    int I, int F, double2* bound) {
+                                                    int I, int F, double2* bound, unsigned* status) {
   const int KE = k_per_block(wk), kb = blockIdx.x, e = blockIdx.y, parts = 256 / KE;
   const void* w = blockIdx.z ? w3 : w1;
   const float* s = blockIdx.z ? s3 : s1;
@@ -562,19 +568,22 @@ __global__ void __launch_bounds__(256) k_moe_bounds(const void* w1, const void* 
   sums[threadIdx.x] = q;
   __syncthreads();
   if (threadIdx.x == 0) {
-    double m = 0.0;
+    double m = 0.0, low = INFINITY;
     for (int k = 0; k < KE; ++k) {
       double t = 0.0;
       for (int p = 0; p < parts; ++p) t += sums[p * KE + k];
       m = fmax(m, t);
+      if (t > 0.0) low = fmin(low, t);
     }
+    if (m > kSpread * kSpread * low) atomicOr(status, 2u);
     double* b = reinterpret_cast<double*>(bound + (size_t)e * gridDim.x + kb);
     b[blockIdx.z] = sqrt(m);
   }
 }
 cudaError_t launch_moe_bounds(const void* w1, const void* w3, const float* s1, const float* s3, int wk, int E, int I, int F,
-                              double2* bound, cudaStream_t s) {
-  k_moe_bounds<<<dim3((unsigned)cdiv(F, k_per_block(wk)), (unsigned)E, 2), 256, 0, s>>>(w1, w3, s1, s3, wk, I, F, bound);
+                              double2* bound, unsigned* status, cudaStream_t s) {
+  k_moe_bounds<<<dim3((unsigned)cdiv(F, k_per_block(wk)), (unsigned)E, 2), 256, 0, s>>>(w1, w3, s1, s3, wk, I, F, bound,
+                                                                                           status);
   return cudaGetLastError();
 }
 
@@ -632,6 +641,11 @@ template <int WK, int T, int ODT>
 static cudaError_t all(const MoeCall& c, int sms, cudaStream_t s) {
   using X = XKind<WK, T>;
   using H = HKind<WK, ODT>;
+  // 11 bits reach 2^28 below the bound of a K block's hidden activations, where
+  // typical ones lie 2^9 to 2^12 below their own columns'
+  if constexpr (!H::kBF && ODT == kBF16) {
+    if (c.spread) return all<WK, T, kF16>(c, sms, s);
+  }
   static std::atomic<bool> done[kMaxDevices];
   const size_t smem = (size_t)c.w13.nkb * k_per_block(WK) * 4;
   cudaError_t e = allow(k_moe_router<WK, T>, done, (EFFORT_MAX_IN_DIM + 128) * 4);

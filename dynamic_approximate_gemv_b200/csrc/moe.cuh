@@ -19,6 +19,7 @@ struct MoeCall {
   void* out;
   int odt;
   long long ostride;
+  bool spread;                  // column norms of w1 or w3 differ much within some K block
   const double2* bound;         // [expert][hidden K block] largest column norms of w1 and w3
   // scratch
   char* xop;                    // [tokens] rows of activation blocks (stream.cuh)

@@ -234,6 +234,9 @@ struct Ring {
   }
 };
 
+// The second of two binary16 parts is stored times 2^11 (store_parts), and so are its sums.
+constexpr float kLowUp = 2048.0f, kLowDown = 1.0f / 2048.0f;
+
 // A fragments of one 16-row tile and K block (two cores in shared memory) times
 // the B fragments of NT column tiles, `live` of them in use, added to c.
 // k-step s takes the lane's elements 4 s .. 4 s + 3.
@@ -245,6 +248,8 @@ __device__ __forceinline__ void mma_tile(uint32_t tile, int g, int q, const uint
   const uint4 v0 = lds128(r + c0), v1 = lds128(r + c1), v2 = lds128(r + kCoreBytes + c0), v3 = lds128(r + kCoreBytes + c1);
   const uint32_t lo[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
   const uint32_t hi[8] = {v2.x, v2.y, v2.z, v2.w, v3.x, v3.y, v3.z, v3.w};
+  constexpr bool kLow = PARTS == 2 && WK != kWBF16;
+  float low[kLow ? NT : 1][4] = {};
 #pragma unroll
   for (int s = 0; s < KS; ++s) {
     uint32_t a0, a1, a2, a3;
@@ -261,8 +266,15 @@ __device__ __forceinline__ void mma_tile(uint32_t tile, int g, int q, const uint
     for (int t = 0; t < NT; ++t) {
       if (NT > 1 && t >= live) break;
 #pragma unroll
-      for (int p = 0; p < PARTS; ++p) mma16<WK == kWBF16>(c[t], a0, a1, a2, a3, b[p][t][s][0], b[p][t][s][1]);
+      for (int p = 0; p < PARTS; ++p)
+        mma16<WK == kWBF16>(kLow && p == 1 ? low[kLow ? t : 0] : c[t], a0, a1, a2, a3, b[p][t][s][0], b[p][t][s][1]);
     }
+  }
+  if constexpr (kLow) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[t][e] = fmaf(low[t][e], kLowDown, c[t][e]);
   }
 }
 
@@ -270,7 +282,12 @@ __device__ __forceinline__ void mma_tile(uint32_t tile, int g, int q, const uint
 // Activations meet 16-bit operands in parts: v = p0 + p1 + .., each of 11
 // (binary16) or 8 (bfloat16) significant bits.  For binary16 a K block of a row
 // is first scaled by a power of two into its range, and the inverse stands
-// behind the parts.  The parts lie in the order of the fragments: of a K block
+// behind the parts.  A second binary16 part is scaled by 2^11 once more, so that
+// it ends where the first does: with the block's bound at 2^14 or more the parts
+// hold 11 and 22 bits of what lies up to 2^28 below the bound, and what lies deeper
+// to within 2^-39 and 2^-50 of the bound (with both parts on one scale 22 bits
+// ended at 2^-17, and a column of w1 and one of w3 a thousand times the others left
+// these 8).  The parts lie in the order of the fragments: of a K block
 // of KE elements lane q of a row's four multiplies KE / 4 neighbours, and the
 // 16-byte pieces of the four lanes alternate, so that a warp reads 64 bytes of
 // a row.
@@ -297,7 +314,7 @@ __device__ __forceinline__ void store_parts(uint16_t* at, int stride, float v) {
     } else {
       const __half h = __float2half_rn(v);
       at[p * stride] = __half_as_ushort(h);
-      v -= __half2float(h);
+      v = (v - __half2float(h)) * kLowUp;
     }
   }
 }

@@ -532,13 +532,21 @@ effort_status_t effort_moe_prepare(const effort_moe_weights_t* weights, void* st
  *   bytes, 256-byte aligned, whose contents mean nothing before and after the
  *   call; calls that may overlap on the GPU bring scratch of their own.
  *   A token whose logits hold NaN counts them as lowest; its gates are NaN.
- *   Precision: products of 16-bit and e4m3 values are exact.  x enters the
- *   first products exactly where it is 16 bits wide, an fp32 x in 22 significant
- *   bits (24 with bf16 weights).  The hidden activations silu(a) b enter the
- *   second product in 11 bits where out is bf16, else in 22 (with bf16 weights:
- *   16, and 24 where out is fp32); with binary16 and e4m3 weights those below
- *   2^-26 of |x|^2 times the largest column norms of w1 and w3 (over 64 or 128
- *   hidden units) keep fewer.  Results do not vary from call to call.
+ *   Precision: products of 16-bit and e4m3 values are exact.  With bfloat16 weights
+ *   x enters the first products in 24 bits or exactly, and the hidden activations
+ *   silu(a) b enter the second in 16 bits (24 where out is fp32).  With binary16
+ *   and e4m3 weights values enter in parts of 11 bits that are scaled together
+ *   over a K block, 64 (e4m3: 128) inputs or hidden units of a token.  One part
+ *   holds what is up to 2^28 below the block's bound in full and what is smaller
+ *   to 2^-39 of the bound; two hold 22 bits, and to 2^-50 of the bound:
+ *     x: binary16 exactly, bfloat16 in one part, fp32 in two; the bound is the
+ *       block's largest |x| (or 2^-97);
+ *     hidden activations: two parts; one where out is bfloat16, unless column
+ *       norms of w1 or w3 differ by more than 32 times within a K block; the bound
+ *       is |x|^2 times the largest column norms of w1 and w3 over the block.
+ *   The router's logits are fp32 sums: experts whose logits differ by less than
+ *   their rounding may change places.
+ *   Results do not vary from call to call.
  *   An expert's weights are read from memory once for up to 8 or 16 of its
  *   tokens and again, mostly from L2, for each 8 or 16 more.
  */

@@ -37,7 +37,7 @@ def check(E, x, std1, std3, std2, i=256, f=192, e=2):
     layer.close()
 
 
-@pytest.mark.parametrize("mag", [1e-29, 1e-31, 1e-32, 1e-33])
+@pytest.mark.parametrize("mag", [1e-29, 1e-31, 1e-32, 1e-33, 1e-35])
 def test_tiny_x_under_large_scales(E, mag):
     """The hidden activations' scale comes from the norm of x, however small x is."""
     check(E, mag * randn(9, 3, 256), 1e-12 / mag, 1e-12 / mag, 1e10)
