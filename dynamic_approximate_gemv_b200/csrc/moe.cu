@@ -281,8 +281,6 @@ __global__ void __launch_bounds__(MoeShape<WK, PARTS, ROWS>::kThreads, 1) k_moe_
   using S = MoeShape<WK, PARTS, ROWS>;
   constexpr int NT = S::NT, MT = S::kMT, W = S::kWarps, KE = WK == kWE4M3 ? 128 : 64, KS = KE / 16;
   constexpr int BLK = act_block<KE, PARTS, SCALED>(), HBLK = act_block<KE, HPARTS, HSCALED>();
-  // every K block's sums apart, to be scaled, or all into one
-  constexpr bool kApart = WK == kWE4M3 || SCALED;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   float* red = reinterpret_cast<float*>(smem + S::kRedAt);
@@ -457,16 +455,14 @@ __global__ void __launch_bounds__(MoeShape<WK, PARTS, ROWS>::kThreads, 1) k_moe_
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         if (m >= G.n) break;
-        if constexpr (kApart) {
-          float d[NT][4] = {};
-          mma_tile<WK, NT, PARTS, KS>(at + m * 2 * kCoreBytes, g, q, b, live, d);
+        // the sum of one K block apart, to be scaled, and because the matrix
+        // instruction truncates: over many K blocks that adds up
+        float d[NT][4] = {};
+        mma_tile<WK, NT, PARTS, KS>(at + m * 2 * kCoreBytes, g, q, b, live, d);
 #pragma unroll
-          for (int j = 0; j < NT; ++j)
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[m][j][e] = fmaf(d[j][e], sc[j][e & 1][e >> 1], acc[m][j][e]);
-        } else {
-          mma_tile<WK, NT, PARTS, KS>(at + m * 2 * kCoreBytes, g, q, b, live, acc[m]);
-        }
+          for (int e = 0; e < 4; ++e) acc[m][j][e] = fmaf(d[j][e], sc[j][e & 1][e >> 1], acc[m][j][e]);
       }
       __syncwarp();  // every lane has read the stage
       ask();

@@ -532,7 +532,8 @@ effort_status_t effort_moe_prepare(const effort_moe_weights_t* weights, void* st
  *   bytes, 256-byte aligned, whose contents mean nothing before and after the
  *   call; calls that may overlap on the GPU bring scratch of their own.
  *   A token whose logits hold NaN counts them as lowest; its gates are NaN.
- *   Precision: products of 16-bit and e4m3 values are exact.  With bfloat16 weights
+ *   Precision: products of 16-bit and e4m3 values are exact, and sums are fp32
+ *   (the matrix instructions' own over 64 or 128 terms).  With bfloat16 weights
  *   x enters the first products in 24 bits or exactly, and the hidden activations
  *   silu(a) b enter the second in 16 bits (24 where out is fp32).  With binary16
  *   and e4m3 weights values enter in parts of 11 bits that are scaled together

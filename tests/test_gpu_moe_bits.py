@@ -87,3 +87,27 @@ def test_small_values_of_a_block_of_x_keep_their_bits(E, kind):
     got = layer(x, ids=ids, gates=gates)[0]
     ref, tol = MP.moe(x, *w64, ids, gates, got.dtype, kind)
     R.assert_close(got, ref, tol)
+
+
+def test_long_sums_of_bf16_weights(E):
+    """One large product and then many small ones in a warp's K blocks: a sum that
+    truncates at each instruction would drop every small one."""
+    i, f = 40960, 8
+    w1 = torch.zeros(1, i, f, device="cuda")
+    w1[0, :, 0] = 0.9 * 2.0 ** -27
+    w1[0, :1024:64, 0] = 1 / 16  # the first K block of each of sixteen warps
+    x = torch.ones(1, i, device="cuda")
+    x[0, :1024:64] = 16.0
+    w3 = torch.zeros(1, i, f, device="cuda")
+    w3[0, 1, 0] = 1.0
+    w2 = torch.zeros(1, f, i, device="cuda")
+    w2[0, 0] = 1.0
+    w = [t.bfloat16() for t in (w1, w3, w2)]
+    layer = E.MoeLayer(*w)
+    ids, gates = torch.zeros(1, 1, device="cuda", dtype=torch.int32), torch.ones(1, 1, device="cuda")
+    got = layer(x, ids=ids, gates=gates)[0]
+    a = (x.double() @ w[0][0].double())[0, 0]
+    ref = a * torch.sigmoid(a)
+    # a: four instructions of its K block (10 U each), 40 K blocks of a warp, 16 warps; silu and two roundings 12 U
+    rel = float((got.double() - ref).abs().max() / ref)
+    assert rel <= (4 * 10 + 40 + 16 + 12) * MP.U, rel / MP.U
