@@ -42,6 +42,7 @@ struct TcArgs {
   void* out;
   long long ostride;
   int odt, ots, tiles, cluster;  // ots: tiles along the output columns
+  WaitHook hook;
 };
 
 constexpr int kTurn = 32 * 64;  // 64 bytes of 32 rows
@@ -133,8 +134,8 @@ __device__ __forceinline__ void tmem_load16(uint32_t at, float (&v)[16]) {
 __device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // A wait that gives up at once after the block's first failure.
-__device__ __forceinline__ void tc_wait(uint32_t bar, uint32_t parity, bool& fine) {
-  if (fine) fine = mbar_wait(bar, parity);
+__device__ __forceinline__ void tc_wait(const TcArgs& a, uint32_t bar, uint32_t parity, bool& fine) {
+  if (fine) fine = mbar_wait(bar, parity, a.hook.tries);
 }
 
 // One thread's accumulators to the output: for ROWS C columns of one row, else
@@ -311,13 +312,14 @@ __global__ void __launch_bounds__(TcShape<ROWS, M, N>::kThreads, 1)
     int s = 0, ph = 0;
     if (early == S::kStages)
       for (int n = early; n < mine; ++n, w.step(nkb, a.ots)) {
-        tc_wait(b_free + 8 * s, ph, fine);
+        tc_wait(a, b_free + 8 * s, ph, fine);
         load_w(w, s);
         load_x(w, s);
         if (++s == S::kStages) s = 0, ph ^= 1;
       }
   } else if (warp == 1) {
     // ------------------------------------------------ matrix instructions
+    grid_dep_wait();  // or the waits below would count the time of the kernel before
     // fp32 sums, e4m3 operands, both K-major, N and M
     constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(S::kStepN >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
     const uint64_t a0 = smem_desc(sbase + S::kHead);
@@ -330,9 +332,9 @@ __global__ void __launch_bounds__(TcShape<ROWS, M, N>::kThreads, 1)
       if constexpr (S::kSteps == 2) ready = mbar_try3(f, ph, r, aph, r + 8, aph);
       else ready = mbar_try2(f, ph, r, aph);
       if (!ready) {
-        tc_wait(f, ph, fine);
+        tc_wait(a, f, ph, fine);
 #pragma unroll
-        for (int h = 0; h < S::kSteps; ++h) tc_wait(r + 8 * h, aph, fine);
+        for (int h = 0; h < S::kSteps; ++h) tc_wait(a, r + 8 * h, aph, fine);
       }
       tc_after();
       const uint64_t da = a0 + (uint64_t)(s * (S::kStage >> 4)), db = da + (S::kABytes >> 4);
@@ -386,7 +388,7 @@ __global__ void __launch_bounds__(TcShape<ROWS, M, N>::kThreads, 1)
           for (int k = 0; k < S::kBatch; ++k) v[i][k] = there && k < n ? p[k] : 0.0f;
         }
       }
-      if (batch >= S::kBatches) tc_wait(b_sce + 8 * sl, (batch / S::kBatches - 1) & 1, fine);
+      if (batch >= S::kBatches) tc_wait(a, b_sce + 8 * sl, (batch / S::kBatches - 1) & 1, fine);
       float* t = reinterpret_cast<float*>(smem + S::kScaleAt) + sl * S::kBatch * S::kScales;
 #pragma unroll
       for (int i = 0; i < R; ++i)
@@ -405,6 +407,7 @@ __global__ void __launch_bounds__(TcShape<ROWS, M, N>::kThreads, 1)
   } else {
     // ------------------------------------------------ epilogue
     if constexpr (N == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    grid_dep_wait();  // as above
     const int quarter = warp & 3, set = (warp - 4) >> 2;
     const int row = quarter * 32 + lane;  // lane of tensor memory
     const uint32_t tm = tmem + ((uint32_t)(quarter * 32) << 16) + set * S::kCols;
@@ -419,7 +422,7 @@ __global__ void __launch_bounds__(TcShape<ROWS, M, N>::kThreads, 1)
     static_assert(kPieces == 1 || kPieces % 2 == 0, "a step starts in the first half");
     float v[2][kLoads][16];
     auto open = [&]() {  // the next accumulator's first piece
-      tc_wait(b_accf + 8 * as, aph, fine);
+      tc_wait(a, b_accf + 8 * as, aph, fine);
       tc_after();
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) tmem_load16(tm + as * S::kStepN + 16 * i, v[kPieces == 1][i]);
@@ -434,7 +437,7 @@ __global__ void __launch_bounds__(TcShape<ROWS, M, N>::kThreads, 1)
         for (int j = 0; j < S::kCols; ++j) acc[h][j] = 0.0f;
       for (int b0 = 0; b0 < seg; b0 += S::kBatch) {
         const int bn = min(S::kBatch, seg - b0);
-        tc_wait(b_scf + 8 * slot, sph, fine);
+        tc_wait(a, b_scf + 8 * slot, sph, fine);
         uint32_t sc = sbase + S::kScaleAt + slot * S::kBatch * S::kScales * 4 + (ROWS ? row * 4 : 0);
         for (int i = 0; i < bn; ++i, sc += S::kScales * 4) {
           const bool more = n + b0 + i + 1 < mine;
@@ -593,7 +596,7 @@ static cudaError_t launch_tc(const TileMat& w, const float* ws, int I, int O, co
   const int ots = cdiv(O, S::kTileCols), nkb = w.nkb;
   const long long tiles = (long long)ots * cdiv(rows, S::kTileRows);
   if (tiles > 0x7fffffffll) return cudaErrorInvalidValue;
-  TcArgs a = {w, ws, align4(nkb), O, rows, xs, xsstride, out, ostride, odt, ots, (int)tiles, 1};
+  TcArgs a = {w, ws, align4(nkb), O, rows, xs, xsstride, out, ostride, odt, ots, (int)tiles, 1, wait_hook()};
   // the cluster size whose longest share of units is shortest; the join is
   // counted as eight of them
   long long best = 0;

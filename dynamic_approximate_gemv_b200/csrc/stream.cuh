@@ -20,11 +20,35 @@
 // long as both operands agree: lane q of a row's four takes 32 consecutive
 // bytes, which are two 16-byte reads that meet no bank twice.
 #pragma once
+#include <stdlib.h>
+
 #include "ffn_common.cuh"
 
 namespace effort {
 
 constexpr int kMaxWaits = 1 << 18;  // tries of a wait before it gives up
+
+// The debug build lets a test make waits run out: EFFORT_TEST_WAIT_TRIES is the
+// number of tries, and with EFFORT_TEST_LOST_COPY=n the n-th and later stages of a
+// ring wait for 16 bytes that no copy brings.
+#ifdef EFFORT_DEBUG
+struct WaitHook {
+  int tries = kMaxWaits, after = 0x7fffffff;
+  __host__ __device__ int lost(int n) const { return n >= after ? 16 : 0; }
+};
+inline WaitHook wait_hook() {
+  WaitHook h;
+  if (const char* t = getenv("EFFORT_TEST_WAIT_TRIES")) h.tries = atoi(t);
+  if (const char* t = getenv("EFFORT_TEST_LOST_COPY")) h.after = atoi(t);
+  return h;
+}
+#else
+struct WaitHook {
+  static constexpr int tries = kMaxWaits;
+  __host__ __device__ static constexpr int lost(int) { return 0; }
+};
+inline WaitHook wait_hook() { return {}; }
+#endif
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
@@ -43,13 +67,13 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 // Bounded: false once the phase did not come.
-__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity) {
-  for (int i = 0; i < kMaxWaits; ++i)
+__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, int tries) {
+  for (int i = 0; i < tries; ++i)
     if (mbar_try(bar, parity)) return true;
   return false;
 }
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
-  return mbar_try(bar, parity) || mbar_wait_long(bar, parity);
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int tries = kMaxWaits) {
+  return mbar_try(bar, parity) || mbar_wait_long(bar, parity, tries);
 }
 // A ready barrier takes 129 clocks to say so (B200, one warp), but several asked
 // together take no longer: whether all are in their phases.

@@ -1,0 +1,71 @@
+"""Waits inside the feed-forward kernels: they do not count the time of the kernel
+before, and one that runs out leaves NaN, never a wrong number.  In child
+processes with the debug build, whose environment variables shorten the waits
+and let them run out (every one of them ends by itself)."""
+import os
+import subprocess
+import sys
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+HEAD = """
+import os, sys, torch
+sys.path.insert(0, {root!r}); sys.path.insert(0, {root!r} + "/tests")
+import dynamic_approximate_gemv_b200 as E
+import ffn_reference as R
+g = torch.Generator("cuda").manual_seed(1)
+randn = lambda *s: torch.randn(*s, device="cuda", generator=g)
+"""
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from dynamic_approximate_gemv_b200 import build
+    build.build()
+
+
+def child(code, *args):
+    env = dict(os.environ, EFFORT_DEBUG_LIB="1")
+    r = subprocess.run([sys.executable, "-c", HEAD.format(root=ROOT) + code, *map(str, args)], env=env, capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and "ok" in r.stdout, r.stdout[-2000:] + r.stderr[-3000:]
+
+
+BEHIND_A_LONG_KERNEL = """
+# A kernel of another program's that lets its successor start at once and then takes 0.2 s (its loop is bounded).
+# One of its blocks leaves the other SMs to the product, whose waits have 20000 tries: a few ms.
+source = r'''
+extern "C" __global__ void lingering(long long ns) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  long long t0, t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
+  for (int i = 0; i < 1 << 28; ++i) {
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    if (t - t0 > ns) break;
+  }
+}
+'''
+lingering = torch.cuda._compile_kernel(source, "lingering")
+rows, i, o = map(int, sys.argv[1:])
+m = E.Fp8Matrix(*R.quantise_weights(0.05 * randn(i, o)))
+q, s = E.quantize_e4m3(randn(rows, i))
+ref = m.matmul(q, s, out_dtype=torch.float32)
+torch.cuda.synchronize()
+os.environ["EFFORT_TEST_WAIT_TRIES"] = "20000"
+lingering(grid=(1, 1, 1), block=(32, 1, 1), args=[200_000_000])
+out = m.matmul(q, s, out_dtype=torch.float32)
+torch.cuda.synchronize()
+assert torch.equal(out, ref), torch.isnan(out).float().mean()
+print("ok")
+"""
+
+
+@pytest.mark.parametrize("rows,i,o", [(4, 512, 512), (12, 2048, 4096), (40, 1024, 512), (200, 1024, 512), (1300, 512, 2560)])
+def test_product_behind_a_long_kernel(rows, i, o):
+    child(BEHIND_A_LONG_KERNEL, rows, i, o)
