@@ -63,7 +63,7 @@ struct TcShape {
   static constexpr int kSets = kEpiWarps / 4, kCols = kStepN / kSets;  // of one epilogue thread in one step
   static constexpr int kBatch = 8, kBatches = N == 256 ? 2 : 3;  // K blocks whose scales are turned at once
   static constexpr bool kJoins = N <= 128;
-  static constexpr int kHead = 1024;
+  static constexpr int kHead = 1024, kBlocksAt = kHead - 9 * 8;
   // the table of scales of one K block: for ROWS each row's for the 128 columns
   // of each half, else each row's
   static constexpr int kScales = ROWS ? M * (N / 128) : N;
@@ -78,6 +78,9 @@ struct TcShape {
   static constexpr int kScaleAt = kHead + kStages * kStage, kJoinAt = kScaleAt + kScaleBytes,
                        kTurnAt = kJoinAt + kJoinBytes;
   static constexpr size_t kSmem = kTurnAt + kTurnBytes;
+  // in the head: the barriers, where tensor memory starts, and whether a wait ran out
+  static constexpr int kTmemAt = 8 * (2 * kStages + 2 * kAcc + 2 * kBatches + 1), kBadAt = kTmemAt + 8;
+  static_assert(kBadAt + 8 <= kBlocksAt, "the head");
   // parts to join: the first tile's has its own place, the last tile's is
   // written when every stage has been used and lies over them
   __host__ __device__ static constexpr int part(int slot) { return slot == 0 ? kJoinAt : kHead; }
@@ -133,7 +136,10 @@ __device__ __forceinline__ void tmem_load16(uint32_t at, float (&v)[16]) {
 }
 __device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// A wait that gives up at once after the block's first failure.
+// A wait that gives up at once after this thread's first failure.  The copying,
+// matrix and scale warps set *bad before they go on, so that the epilogue stores
+// no tile as good from then on; its own failures it knows.  (A store in this
+// function instead cost 5%: 307 against 293 us at 4096 x 4096 x 14336.)
 __device__ __forceinline__ void tc_wait(const TcArgs& a, uint32_t bar, uint32_t parity, bool& fine) {
   if (fine) fine = mbar_wait(bar, parity, a.hook.tries);
 }
@@ -244,14 +250,15 @@ __global__ void __launch_bounds__(TcShape<ROWS, M, N>::kThreads, 1)
   // barriers: stage full / free, accumulator full / read, scales full / read
   const uint32_t b_full = sbase, b_free = b_full + 8 * S::kStages, b_accf = b_free + 8 * S::kStages,
                  b_acce = b_accf + 8 * S::kAcc, b_scf = b_acce + 8 * S::kAcc, b_sce = b_scf + 8 * S::kBatches,
-                 tmem_at = b_sce + 8 * S::kBatches;
-  volatile int* bad = reinterpret_cast<volatile int*>(smem + (tmem_at + 8 - sbase));  // some wait ran out
-  int2* from = reinterpret_cast<int2*>(smem + S::kHead - 9 * sizeof(int2));
+                 b_end = b_sce + 8 * S::kBatches;  // b_end: all products done, after a failure
+  volatile int* bad = reinterpret_cast<volatile int*>(smem + S::kBadAt);
+  int2* from = reinterpret_cast<int2*>(smem + S::kBlocksAt);
   if (threadIdx.x >= 32 && threadIdx.x <= 32 + cl) {
     const long long u = units * (threadIdx.x - 32) / cl;
     from[threadIdx.x - 32] = make_int2((int)(u / nkb), (int)(u % nkb));
   }
   if (threadIdx.x == 0) {
+    mbar_init(b_end, 1);
     asm volatile("prefetch.tensormap [%0];" ::"l"(&xmap) : "memory");
     *bad = 0;
     for (int i = 0; i < S::kStages; ++i) {
@@ -270,15 +277,16 @@ __global__ void __launch_bounds__(TcShape<ROWS, M, N>::kThreads, 1)
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tmem_at), "n"(S::kTmemCols)
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sbase + S::kTmemAt), "n"(S::kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   tc_before();
   __syncthreads();
   tc_after();
-  const uint32_t tmem = *reinterpret_cast<const uint32_t*>(smem + (tmem_at - sbase));
+  const uint32_t tmem = *reinterpret_cast<const uint32_t*>(smem + S::kTmemAt);
   bool fine = true;
+  int asked = 0;  // stages the copying lane has asked for
   // the widest shape: 384 threads launched with 168 registers; 8 x 32 x 208 + 4 x
   // 32 x 80 fit in them
   if constexpr (N == 256) {
@@ -292,7 +300,7 @@ __global__ void __launch_bounds__(TcShape<ROWS, M, N>::kThreads, 1)
     // (one lane: the copies take their operands from the warp's uniform registers)
     const int last_group = a.w.cores / kGroupCores - 1;  // columns behind it are not stored: any weights do
     auto load_w = [&](const Walk& w, int s) {
-      mbar_expect(b_full + 8 * s, S::kStage);
+      mbar_expect(b_full + 8 * s, S::kStage + a.hook.lost(asked++));
 #pragma unroll
       for (int h = 0; h < S::kTileCols / 64; ++h)
         bulk_load(sbase + S::kHead + s * S::kStage + (ROWS ? S::kABytes : 0) + h * kGroupBytes,
@@ -313,6 +321,10 @@ __global__ void __launch_bounds__(TcShape<ROWS, M, N>::kThreads, 1)
     if (early == S::kStages)
       for (int n = early; n < mine; ++n, w.step(nkb, a.ots)) {
         tc_wait(a, b_free + 8 * s, ph, fine);
+        if (!fine) {  // the stage may still be read, or not have come
+          *bad = 1;
+          break;
+        }
         load_w(w, s);
         load_x(w, s);
         if (++s == S::kStages) s = 0, ph ^= 1;
@@ -324,6 +336,7 @@ __global__ void __launch_bounds__(TcShape<ROWS, M, N>::kThreads, 1)
     constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(S::kStepN >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
     const uint64_t a0 = smem_desc(sbase + S::kHead);
     const uint32_t e = elect();
+    uint32_t frees = e;  // whether this lane hands stages back: none after a failure, so no copy meets another
     int s = 0, ph = 0, as = 0, aph = 1;  // aph: an accumulator's first use waits for nothing
     for (int n = 0; n < mine; ++n) {
       // the stage and the K block's accumulators (kAcc is a multiple of kSteps)
@@ -335,6 +348,10 @@ __global__ void __launch_bounds__(TcShape<ROWS, M, N>::kThreads, 1)
         tc_wait(a, f, ph, fine);
 #pragma unroll
         for (int h = 0; h < S::kSteps; ++h) tc_wait(a, r + 8 * h, aph, fine);
+        if (!fine) {
+          *bad = 1;
+          frees = 0;
+        }
       }
       tc_after();
       const uint64_t da = a0 + (uint64_t)(s * (S::kStage >> 4)), db = da + (S::kABytes >> 4);
@@ -347,7 +364,7 @@ __global__ void __launch_bounds__(TcShape<ROWS, M, N>::kThreads, 1)
         for (int k = 1; k < 4; ++k) mma_f8<true>(e, d, da + 2 * k, dh + 2 * k, idesc);
         mma_commit(e, b_accf + 8 * (as + h));
       }
-      mma_commit(e, b_free + 8 * s);
+      mma_commit(frees, b_free + 8 * s);
       as += S::kSteps;
       if (as == S::kAcc) as = 0, aph ^= 1;
       if (++s == S::kStages) s = 0, ph ^= 1;
@@ -389,6 +406,7 @@ __global__ void __launch_bounds__(TcShape<ROWS, M, N>::kThreads, 1)
         }
       }
       if (batch >= S::kBatches) tc_wait(a, b_sce + 8 * sl, (batch / S::kBatches - 1) & 1, fine);
+      if (!fine) *bad = 1;
       float* t = reinterpret_cast<float*>(smem + S::kScaleAt) + sl * S::kBatch * S::kScales;
 #pragma unroll
       for (int i = 0; i < R; ++i)
@@ -526,6 +544,21 @@ __global__ void __launch_bounds__(TcShape<ROWS, M, N>::kThreads, 1)
   if (warp != 2) grid_dep_launch();
   tc_before();
   __syncthreads();
+  const bool failed = *bad;  // the same in every thread
+  if (failed) {
+    // copies and products in flight end before the block does (as long as a wait
+    // lasts), and its parts say that they are none
+    if (threadIdx.x == 0)
+      for (int i = max(0, asked - S::kStages); i < asked && mbar_wait(b_full + 8 * (i % S::kStages), i / S::kStages & 1, a.hook.tries);) ++i;
+    if (warp == 1) {
+      mma_commit(elect(), b_end);
+      mbar_wait(b_end, 0, a.hook.tries);
+    }
+    __syncthreads();
+    if constexpr (S::kJoins)
+      for (int i = threadIdx.x; i < S::kPart / 4; i += S::kThreads)
+        for (int slot = 0; slot < 2; ++slot) reinterpret_cast<float*>(smem + S::part(slot))[i] = __int_as_float(0x7fffffff);
+  }
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kTmemCols));
   if (!S::kJoins || cl == 1) return;
   cluster_sync();

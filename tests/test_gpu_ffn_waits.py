@@ -69,3 +69,35 @@ print("ok")
 @pytest.mark.parametrize("rows,i,o", [(4, 512, 512), (12, 2048, 4096), (40, 1024, 512), (200, 1024, 512), (1300, 512, 2560)])
 def test_product_behind_a_long_kernel(rows, i, o):
     child(BEHIND_A_LONG_KERNEL, rows, i, o)
+
+
+LOST = """
+# From the given stage of every block's ring on, 16 bytes are waited for that never come.
+rows, i, o, after = map(int, sys.argv[1:])
+m = E.Fp8Matrix(*R.quantise_weights(0.05 * randn(i, o)))
+q, s = E.quantize_e4m3(randn(rows, i))
+ref = m.matmul(q, s, out_dtype=torch.float32)
+torch.cuda.synchronize()
+os.environ["EFFORT_TEST_WAIT_TRIES"] = "20000"
+os.environ["EFFORT_TEST_LOST_COPY"] = str(after)
+out = m.matmul(q, s, out_dtype=torch.float32)
+torch.cuda.synchronize()
+nan = torch.isnan(out)
+assert torch.equal(out[~nan], ref[~nan])
+print("NaN", float(nan.float().mean()))
+assert nan.all() if after == 0 else nan.any()
+del os.environ["EFFORT_TEST_WAIT_TRIES"], os.environ["EFFORT_TEST_LOST_COPY"]
+assert torch.equal(m.matmul(q, s, out_dtype=torch.float32), ref)
+torch.cuda.synchronize()
+print("ok")
+"""
+
+
+# clusters with joined parts (up to 64 rows, and 128 x 128 tiles), and 128 x 256 tiles of several rounds; `after` is
+# below a block's share of K blocks in each
+@pytest.mark.parametrize("rows,i,o,after", [(12, 2048, 4096, 0), (12, 2048, 4096, 2), (30, 4096, 300, 1), (64, 4096, 14336, 0),
+                                            (64, 4096, 14336, 13), (200, 4091, 1003, 2), (1024, 1024, 4096, 5),
+                                            (2000, 2048, 8192, 0), (2000, 2048, 8192, 20)])
+def test_product_whose_waits_run_out(rows, i, o, after):
+    """Every output is right or NaN, and the next call is right."""
+    child(LOST, rows, i, o, after)
