@@ -95,6 +95,7 @@ struct FewRows {
   void* out;
   long long ostride;
   int odt, tiles, cluster, kw;
+  WaitHook hook;
 };
 constexpr int kFewRowsMax = 16;
 constexpr int kFewExtra = 12 * 1024;  // the table of x's scales
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(FewShape<NT>::kThreads, 1) k_fp8_few_rows(cons
     const int n1 = min(n, 4 - (t & 3));               // tiles up to the end of 64 stored rows
     const bool two = (t + n - 1) / 8 > t / 8;         // whether the tiles lie in two blocks of 128 columns
     if (lane == 0) {
-      mbar_expect(bar, n * 2 * kCoreBytes + a.rows * xb + (two ? 32 : 16));
+      mbar_expect(bar, n * 2 * kCoreBytes + a.rows * xb + (two ? 32 : 16) + a.hook.lost(ring.put));
       bulk_load(buf, a.w.data + core_at(2 * t, kb, a.w.nkb), n1 * 2 * kCoreBytes, bar);
       if (n1 < n)
         bulk_load(buf + n1 * 2 * kCoreBytes, a.w.data + core_at(2 * (t + n1), kb, a.w.nkb), (n - n1) * 2 * kCoreBytes, bar);
@@ -178,7 +179,6 @@ __global__ void __launch_bounds__(FewShape<NT>::kThreads, 1) k_fp8_few_rows(cons
   __syncthreads();
 
   const int live = NT == 1 ? 1 : (a.rows + 7) / 8;
-  bool fine = true;
   for (int gi = wr; gi < groups; gi += rw) {
     const int t = t0 + gi * MT, n = min(MT, t1 - t);
     float acc[MT][NT][4];
@@ -189,8 +189,7 @@ __global__ void __launch_bounds__(FewShape<NT>::kThreads, 1) k_fp8_few_rows(cons
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.0f;
     for (int kb = kb0 + wk; kb < kb1; kb += kw) {
-      uint32_t at;
-      fine &= ring.wait(&at);
+      const uint32_t at = ring.wait(smem, warp, a.hook, [&]() { pg = groups; });
       uint32_t b[1][NT][8][2];
       float sx[NT][2];
 #pragma unroll
@@ -222,7 +221,7 @@ __global__ void __launch_bounds__(FewShape<NT>::kThreads, 1) k_fp8_few_rows(cons
     // join the warps' sums (and the cluster's)
     set_sync(wr, kw);
     float* mine = red + warp * S::kRed;
-    const float poison = fine ? 0.0f : __int_as_float(0x7fffffff);
+    const float poison = ring.fine ? 0.0f : __int_as_float(0x7fffffff);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -262,6 +261,7 @@ __global__ void __launch_bounds__(FewShape<NT>::kThreads, 1) k_fp8_few_rows(cons
       cluster_sync();  // the sums may be written over (and, at the end, the block may leave)
     }
   }
+  ring.drain(smem, warp, lane, a.hook);
 }
 
 // Blocks of `cluster` that fit the device at once (one block per SM).
@@ -356,7 +356,7 @@ cudaError_t launch_fp8_matmul(const TileMat& w, const float* ws, int I, int O, c
   const int most = w.nkb > 1536 ? 8 : kFewRowsMax;
   for (int64_t r = 0; r < rows; r += most) {
     FewRows a = {w, ws, align4(w.nkb), I, O, (int)(rows - r < most ? rows - r : most), x + r * xstride,
-                 xstride, xs + r * xsstride, xsstride, (char*)out + r * ostride * osz, ostride, odt, cdiv(O, 16), 1, 1};
+                 xstride, xs + r * xsstride, xsstride, (char*)out + r * ostride * osz, ostride, odt, cdiv(O, 16), 1, 1, wait_hook()};
     cudaError_t e = a.rows <= 8 ? launch_few_rows<1>(a, s) : launch_few_rows<2>(a, s);
     if (e != cudaSuccess) return e;
   }

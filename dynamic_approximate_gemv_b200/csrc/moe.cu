@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(MoeShape<WK, PARTS, ROWS>::kThreads, 1) k_moe_
     const uint32_t buf = ring.next_buf(), bar = ring.next_bar();
     constexpr int kScales = WK == kWE4M3 ? (DOWN ? 1 : 2) : 0;
     if (lane == 0) {
-      mbar_expect(bar, P.n * 2 * kCoreBytes + P.count * BLK + 16 * kScales);
+      mbar_expect(bar, P.n * 2 * kCoreBytes + P.count * BLK + 16 * kScales + c.hook.lost(ring.put));
       bulk_load(buf, w.data + P.expert * w.stride + core_at(2 * P.t, pk, nkb), P.n * 2 * kCoreBytes, bar);
     }
     __syncwarp();
@@ -414,7 +414,6 @@ __global__ void __launch_bounds__(MoeShape<WK, PARTS, ROWS>::kThreads, 1) k_moe_
 #pragma unroll 1
   for (int s = 0; s < S::kStages; ++s) ask();
 
-  bool fine = true;
   for (Cursor cu = first; cu.u < u1; step(cu)) {
     const Group G = group_at(cu);
     const int live = NT == 1 ? 1 : (G.count + 7) / 8;
@@ -428,8 +427,7 @@ __global__ void __launch_bounds__(MoeShape<WK, PARTS, ROWS>::kThreads, 1) k_moe_
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.0f;
     for (int kb = G.kb0 + wk; kb < G.kb1; kb += kw) {
-      uint32_t at;
-      fine &= ring.wait(&at);
+      const uint32_t at = ring.wait(smem, warp, c.hook, [&]() { pc.u = u1; });
       uint32_t b[PARTS][NT][KS][2];
       float sc[NT][2][2];  // the scales of column 2 q + e and the tile's rows g, g + 8: x's is a power of two
 #pragma unroll
@@ -470,7 +468,7 @@ __global__ void __launch_bounds__(MoeShape<WK, PARTS, ROWS>::kThreads, 1) k_moe_
     // join the set's sums
     set_sync(set, kw);
     float* mine = red + warp * S::kRed;
-    const float poison = fine ? 0.0f : __int_as_float(0x7fffffff);
+    const float poison = ring.fine ? 0.0f : __int_as_float(0x7fffffff);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -518,6 +516,7 @@ __global__ void __launch_bounds__(MoeShape<WK, PARTS, ROWS>::kThreads, 1) k_moe_
       }
     }
   }
+  ring.drain(smem, warp, lane, c.hook);
 }
 
 // out[t] = sum over its pairs and the K shares, in order
@@ -704,6 +703,7 @@ size_t moe_scratch(MoeCall* c, char* base, int n_tokens, int top_k, int n_expert
     c->xpitch = xpitch;
     c->hpitch = hpitch;
     c->shares = shares;
+    c->hook = wait_hook();
   }
   return at;
 }

@@ -1,6 +1,6 @@
 // What one mixture-of-experts call hands to its kernels.
 #pragma once
-#include "ffn_common.cuh"
+#include "stream.cuh"
 
 namespace effort {
 
@@ -27,6 +27,7 @@ struct MoeCall {
   char* h;                      // [pairs] hidden activations, likewise
   float* z;                     // [K share][pairs][I] second products
   int xpitch, hpitch, shares;   // bytes of a row; parts of the second product's K
+  WaitHook hook;
 };
 
 // scratch of a call in bytes, carved into c where c is given (base: the caller's memory)

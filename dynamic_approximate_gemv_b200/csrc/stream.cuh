@@ -234,11 +234,14 @@ struct StreamShape {
   static constexpr size_t kSmem = kExtraAt + EXTRA;
 };
 
-// One warp's ring.
+// One warp's ring.  A warp whose wait ran out (fine is false) asks for nothing more;
+// its sums are to be poisoned, and drain() lets the copies that are in flight end
+// before the block does.  Its lanes vote on each wait, so that they stay together.
 template <typename S>
 struct Ring {
   uint32_t buf, bar;
   int put = 0, got = 0;  // stages asked for and taken
+  bool fine = true;
   __device__ void init(uint32_t sbase, int warp, int lane) {
     buf = sbase + S::kRingAt + warp * S::kStages * S::kStage;
     bar = sbase + warp * S::kStages * 8;
@@ -249,13 +252,27 @@ struct Ring {
   }
   __device__ uint32_t next_buf() const { return buf + (put % S::kStages) * S::kStage; }
   __device__ uint32_t next_bar() const { return bar + (put % S::kStages) * 8; }
-  __device__ bool wait(uint32_t* at) {
-    const int s = got % S::kStages;
-    *at = buf + s * S::kStage;
-    const bool ok = mbar_wait(bar + s * 8, (got / S::kStages) & 1);
+  // the next stage; stop() after a failure sees to it that no more are asked for
+  template <typename F>
+  __device__ uint32_t wait(uint8_t* smem, int warp, WaitHook hook, F&& stop) {
+    const int s = got % S::kStages, parity = (got / S::kStages) & 1;
+    if (!__all_sync(~0u, mbar_try(bar + s * 8, parity)) && fine &&
+        !__all_sync(~0u, mbar_wait_long(bar + s * 8, parity, hook.tries))) {
+      reinterpret_cast<int2*>(smem + kLateAt)[warp] = make_int2(got, put);
+      fine = false;
+      stop();
+    }
     ++got;
-    return ok;
+    return buf + s * S::kStage;
   }
+  __device__ void drain(const uint8_t* smem, int warp, int lane, WaitHook hook) const {
+    if (lane != 0 || fine) return;
+    const int2 late = reinterpret_cast<const int2*>(smem + kLateAt)[warp];
+    for (int i = late.x; i < late.y && mbar_wait(bar + i % S::kStages * 8, (i / S::kStages) & 1, hook.tries); ++i) {}
+  }
+  // behind the barriers: the stages that each warp had got and asked for when its wait ran out
+  static constexpr int kLateAt = S::kWarps * S::kStages * 8;
+  static_assert(kLateAt + S::kWarps * 8 <= kStreamHead, "the head");
 };
 
 // The second of two binary16 parts is stored times 2^11 (store_parts), and so are its sums.

@@ -93,11 +93,47 @@ print("ok")
 """
 
 
-# clusters with joined parts (up to 64 rows, and 128 x 128 tiles), and 128 x 256 tiles of several rounds; `after` is
+# few rows on the rings of stream.cuh (alone and in clusters); clusters with joined parts (up to 64 rows, and 128 x 128 tiles), and 128 x 256 tiles of several rounds; `after` is
 # below a block's share of K blocks in each
-@pytest.mark.parametrize("rows,i,o,after", [(12, 2048, 4096, 0), (12, 2048, 4096, 2), (30, 4096, 300, 1), (64, 4096, 14336, 0),
+@pytest.mark.parametrize("rows,i,o,after", [(1, 512, 512, 0), (1, 4096, 14336, 0), (1, 4096, 14336, 3), (8, 14336, 4096, 2),
+                                            (13, 1000, 500, 0), (3, 40000, 100, 1), (12, 2048, 4096, 0), (12, 2048, 4096, 2), (30, 4096, 300, 1), (64, 4096, 14336, 0),
                                             (64, 4096, 14336, 13), (200, 4091, 1003, 2), (1024, 1024, 4096, 5),
                                             (2000, 2048, 8192, 0), (2000, 2048, 8192, 20)])
 def test_product_whose_waits_run_out(rows, i, o, after):
     """Every output is right or NaN, and the next call is right."""
     child(LOST, rows, i, o, after)
+
+
+LOST_MIXTURE = """
+# As above, in the mixture's products: what a lost copy of the first leaves goes through the second.
+kind, dt, tokens, after = sys.argv[1], *map(int, sys.argv[2:])
+e, i, f = 4, 1024, 1792
+w = [0.05 * randn(e, *d) for d in ((i, f), (i, f), (f, i))]
+scales = None
+if kind == "e4m3":
+    w, scales = zip(*(R.quantise_weights(t) for t in w))
+else:
+    w = [t.to({{"f16": torch.float16, "bf16": torch.bfloat16}}[kind]) for t in w]
+layer = E.MoeLayer(*w, scales=scales, router=randn(e, i))
+x = randn(tokens, i).to([torch.float32, torch.bfloat16][dt])
+ref = layer(x, top_k=2)[0]
+torch.cuda.synchronize()
+os.environ["EFFORT_TEST_WAIT_TRIES"] = "20000"
+os.environ["EFFORT_TEST_LOST_COPY"] = str(after)
+out = layer(x, top_k=2)[0]
+torch.cuda.synchronize()
+nan = torch.isnan(out)
+assert torch.equal(out[~nan], ref[~nan])
+print("NaN", float(nan.float().mean()))
+assert nan.any() and (after or nan.all())
+del os.environ["EFFORT_TEST_WAIT_TRIES"], os.environ["EFFORT_TEST_LOST_COPY"]
+assert torch.equal(layer(x, top_k=2)[0], ref)
+torch.cuda.synchronize()
+print("ok")
+""".replace("{{", "{").replace("}}", "}")
+
+
+@pytest.mark.parametrize("kind,dt,tokens,after", [("e4m3", 0, 1, 0), ("e4m3", 1, 7, 1), ("f16", 0, 1, 1), ("f16", 1, 20, 0),
+                                                  ("bf16", 0, 40, 2), ("bf16", 1, 3, 0)])
+def test_mixture_whose_waits_run_out(kind, dt, tokens, after):
+    child(LOST_MIXTURE, kind, dt, tokens, after)
