@@ -316,12 +316,13 @@ __global__ void __launch_bounds__(W * 32) k_block_norm(const effort_block_norm_t
 // with gate and e4m3).
 // KEEP: the weights are of type T.
 template <typename T, int W, int S, bool KEEP>
-__global__ void __launch_bounds__(W * 32, 24 / W) k_block_norm_rows(const effort_block_norm_t a) {
+__global__ void __launch_bounds__(W * 32, 24 / W) k_block_norm_rows(const effort_block_norm_t a, const WaitHook hook) {
   using L = Lay<T, true>;
   constexpr int E = L::E;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float red[2][W];
   __shared__ uint64_t bars[2];
+  __shared__ long long late;  // the row at which the copying thread's wait ran out
   const int lane = threadIdx.x & 31, warp = warp_index(), n = (int)a.dim;
   const float inv_n = __fdiv_rn(1.0f, (float)n);
   const bool gates = a.gate && a.gate_stride != 0;
@@ -330,6 +331,7 @@ __global__ void __launch_bounds__(W * 32, 24 / W) k_block_norm_rows(const effort
   BlockSum<W> sum{red, lane, warp, 0};
   auto col = [&](int s) { return (s * W + warp) * 32 * E + lane * E; };
   if (threadIdx.x == 0) {
+    late = -1;
     mbar_init(bar, 1);
     mbar_init(bar + 8, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -338,10 +340,12 @@ __global__ void __launch_bounds__(W * 32, 24 / W) k_block_norm_rows(const effort
   __syncthreads();
   grid_dep_launch();
   grid_dep_wait();
+  bool fine = true;  // no wait of this thread has run out
+  int asked = 0;
   auto ask = [&](long long r, int st) {  // x, y and the gate's row, one after another
-    if (threadIdx.x != 0 || r >= a.rows) return;
+    if (threadIdx.x != 0 || r >= a.rows || !fine) return;
     const uint32_t to = sbase + st * arrays * bytes;
-    mbar_expect(bar + 8 * st, arrays * bytes);
+    mbar_expect(bar + 8 * st, arrays * bytes + hook.lost(asked++));
     bulk_load(to, static_cast<const T*>(a.x) + r * a.x_stride, bytes, bar + 8 * st);
     if (a.y) bulk_load(to + bytes, static_cast<const T*>(a.y) + r * a.y_stride, bytes, bar + 8 * st);
     if (gates) bulk_load(to + (arrays - 1) * bytes, static_cast<const T*>(a.gate) + r * a.gate_stride, bytes, bar + 8 * st);
@@ -420,10 +424,9 @@ __global__ void __launch_bounds__(W * 32, 24 / W) k_block_norm_rows(const effort
       }
     }
   };
-  bool fine = true;
   int st = 0, ph = 0;
   for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
-    fine = fine && mbar_wait(bar + 8 * st, ph);
+    fine = fine && mbar_wait(bar + 8 * st, ph, hook.tries);
     const T* in = reinterpret_cast<const T*>(smem + st * arrays * bytes);
     float v[S][E];
     // one array's values of slot s
@@ -459,6 +462,7 @@ __global__ void __launch_bounds__(W * 32, 24 / W) k_block_norm_rows(const effort
       }
     }
     if (!fine) {
+      if (threadIdx.x == 0 && late < 0) late = r;
 #pragma unroll
       for (int s = 0; s < S; ++s)
 #pragma unroll
@@ -484,6 +488,12 @@ __global__ void __launch_bounds__(W * 32, 24 / W) k_block_norm_rows(const effort
     }
     ph ^= st;
     st ^= 1;
+  }
+  // copies in flight end before the block does
+  if (threadIdx.x == 0 && !fine) {
+    const int k = (int)((late - blockIdx.x) / gridDim.x);  // that row among the block's: it and the next were asked for
+    for (int i = k; i < k + 2 && blockIdx.x + (long long)gridDim.x * i < a.rows; ++i)
+      mbar_wait(bar + 8 * (i & 1), i >> 1 & 1, hook.tries);
   }
 }
 
@@ -514,7 +524,7 @@ static cudaError_t go_rows_as(const effort_block_norm_t& a, int sms, cudaStream_
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_block_norm_rows<T, W, S, KEEP>, a);
+  return cudaLaunchKernelEx(&cfg, k_block_norm_rows<T, W, S, KEEP>, a, wait_hook());
 }
 
 template <typename T, int W, int ES>

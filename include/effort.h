@@ -376,6 +376,9 @@ effort_status_t effort_device_bytes_held(uint64_t* bytes);
  *  - No call allocates, synchronises or keeps anything between calls: any of
  *    them may run on several streams at once, on one handle too, and may be
  *    captured into a graph.
+ *  - Waits inside the kernels are bounded.  None runs out on a working device;
+ *    where one does, the outputs that hang on it are NaN and the call's status is
+ *    EFFORT_OK all the same.
  *  - rows (n_tokens) may be 0: nothing is launched.  Rows of an output beyond
  *    the call's rows, and elements between dim and the stride, are not touched.
  *  - inf and NaN follow IEEE arithmetic within their own row (token) and reach

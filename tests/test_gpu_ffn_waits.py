@@ -137,3 +137,29 @@ print("ok")
                                                   ("bf16", 0, 40, 2), ("bf16", 1, 3, 0)])
 def test_mixture_whose_waits_run_out(kind, dt, tokens, after):
     child(LOST_MIXTURE, kind, dt, tokens, after)
+
+
+LOST_NORM = """
+rows, dim, after = map(int, sys.argv[1:])
+x, y = randn(rows, dim).bfloat16(), randn(rows, dim).bfloat16()
+call = lambda **kw: E.block_norm(x, y, post="rms", gate=y, pre="layer", **kw)
+ref, refq = call(), call(quantize=True)
+torch.cuda.synchronize()
+os.environ["EFFORT_TEST_WAIT_TRIES"] = "20000"
+os.environ["EFFORT_TEST_LOST_COPY"] = str(after)
+out, outq = call(), call(quantize=True)
+torch.cuda.synchronize()
+for a, b in ((out.x, ref.x), (out.h, ref.h), (outq.scales, refq.scales), (outq.q.float(), refq.q.float())):
+    nan = torch.isnan(a)
+    assert torch.equal(a[~nan], b[~nan]) and nan.any() and (after or nan.all())
+    assert not after or not nan.all()
+del os.environ["EFFORT_TEST_WAIT_TRIES"], os.environ["EFFORT_TEST_LOST_COPY"]
+assert torch.equal(call().h, ref.h)
+torch.cuda.synchronize()
+print("ok")
+"""
+
+
+@pytest.mark.parametrize("rows,dim,after", [(8000, 1024, 0), (8000, 1024, 1), (2000, 4096, 2), (900, 16384, 3)])
+def test_norm_whose_waits_run_out(rows, dim, after):
+    child(LOST_NORM, rows, dim, after)
