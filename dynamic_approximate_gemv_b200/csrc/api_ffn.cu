@@ -52,6 +52,36 @@ size_t dtype_size(int t) { return t == EFFORT_F32 ? 4 : 2; }
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 bool kind_ok(int k) { return k == EFFORT_NORM_NONE || k == EFFORT_NORM_RMS || k == EFFORT_NORM_LAYER; }
 
+// An array of a call: rows of `width` bytes, `stride` bytes apart (at least width).
+struct Span {
+  const void* p;
+  int64_t rows, stride, width;
+};
+
+// Whether two arrays have a byte in common.
+bool meet(const Span& a, const Span& b) {
+  if (!a.p || !b.p) return false;
+  using Wide = __int128;
+  const Wide a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p, d = b0 - a0;
+  if (a0 + (Wide)(a.rows - 1) * a.stride + a.width <= b0 || b0 + (Wide)(b.rows - 1) * b.stride + b.width <= a0) return false;
+  if (a.rows == 1 && b.rows == 1) return true;
+  const Wide sa = a.rows > 1 ? a.stride : b.stride, sb = b.rows > 1 ? b.stride : a.stride;
+  if (sa == sb) {
+    // row i of a, i + k of b: k's least value with d + k s > -b.width, and in b
+    const Wide num = -(Wide)b.width - d;
+    Wide k = num / sa - (num % sa < 0 ? 1 : 0) + 1;
+    if (k < 1 - a.rows) k = 1 - a.rows;
+    return k < b.rows && d + k * sa < a.width;
+  }
+  for (int64_t i = 0, j = 0; i < a.rows && j < b.rows;) {
+    const Wide at = d + j * sb - i * sa;  // b's row seen from a's
+    if (at >= a.width) ++i;
+    else if (at <= -(Wide)b.width) ++j;
+    else return true;
+  }
+  return false;
+}
+
 effort_status_t device_sms(int* sms) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
@@ -102,6 +132,26 @@ effort_status_t effort_block_norm(const effort_block_norm_t* args, void* stream)
     return EFFORT_ERR_ARG;
   if (a.rows > EFFORT_MAX_ROWS || a.dim > EFFORT_MAX_IN_DIM) return EFFORT_ERR_UNSUPPORTED;
   if (a.rows == 0) return EFFORT_OK;
+  const size_t hsz = a.h_out ? dtype_size(a.h_dtype) : 0;
+  auto rows = [&](const void* p, int64_t stride, size_t size) {
+    return Span{p, a.rows, stride * (int64_t)size, a.dim * (int64_t)size};
+  };
+  auto vec = [&](const void* p) { return Span{p, 1, 0, a.dim * (int64_t)wsz}; };
+  const Span in[] = {rows(a.x, a.x_stride, sz), rows(a.y, a.y_stride, sz),
+                     {a.gate, a.gate_stride ? a.rows : 1, a.gate_stride * (int64_t)sz, a.dim * (int64_t)sz},
+                     vec(a.post_weight), vec(a.post_bias), vec(a.pre_weight), vec(a.pre_bias)};
+  const Span out[] = {rows(a.x_out, a.x_out_stride, sz), rows(a.h_out, a.h_stride, hsz), rows(a.q_out, a.q_stride, 1),
+                      {a.q_scales, a.rows, a.q_scales_stride * 4, (a.dim + kBlk - 1) / kBlk * 4}};
+  for (int o = 0; o < 4; ++o) {
+    for (int i = 0; i < 7; ++i) {
+      // x_out and h_out in the place of x or y: an element is read before it is written
+      const bool same = o < 2 && i < 2 && in[i].p == out[o].p && in[i].width == out[o].width &&
+                        (a.rows == 1 || in[i].stride == out[o].stride);
+      if (!same && meet(in[i], out[o])) return EFFORT_ERR_ARG;
+    }
+    for (int i = 0; i < o; ++i)
+      if (meet(out[i], out[o])) return EFFORT_ERR_ARG;
+  }
   int sms = 0;
   effort_status_t st = device_sms(&sms);
   if (st != EFFORT_OK) return st;
@@ -159,6 +209,9 @@ effort_status_t effort_fp8_matmul(effort_fp8_t m, const void* x, int64_t x_strid
   if (!aligned(out, dtype_size(out_dtype)) || out_stride < m->O) return EFFORT_ERR_ARG;
   if (rows > EFFORT_MAX_ROWS) return EFFORT_ERR_UNSUPPORTED;
   if (rows == 0) return EFFORT_OK;
+  const int64_t osz = (int64_t)dtype_size(out_dtype);
+  const Span o = {out, rows, out_stride * osz, m->O * osz};
+  if (meet(o, {x, rows, x_stride, m->I}) || meet(o, {x_scales, rows, x_scales_stride * 4, m->w.nkb * 4})) return EFFORT_ERR_ARG;
   DeviceGuard guard(m->dev);
   return launched(launch_fp8_matmul(m->w, m->ws, (int)m->I, (int)m->O, (const uint8_t*)x, x_stride, x_scales,
                                     x_scales_stride, rows, out_dtype, out, out_stride, (cudaStream_t)stream));
@@ -297,6 +350,14 @@ effort_status_t effort_moe_forward(effort_moe_t h, const void* x, effort_dtype_t
   if (n_tokens == 0) return EFFORT_OK;
   MoeCall c = {};
   if (scratch_bytes < call_scratch(h, nullptr, nullptr, (int)n_tokens, top_k)) return EFFORT_ERR_ARG;
+  const int64_t xsz = (int64_t)dtype_size(x_dtype), osz = (int64_t)dtype_size(out_dtype);
+  const Span sx = {x, n_tokens, x_stride * xsz, h->I * xsz}, so = {out, n_tokens, out_stride * osz, h->I * osz},
+             si = {ids, 1, 0, n_tokens * top_k * 4}, sg = {gates, 1, 0, n_tokens * top_k * 4},
+             ss = {scratch, 1, 0, (int64_t)scratch_bytes};
+  const bool routes = gate_mode != EFFORT_GATE_GIVEN;  // the call writes ids and gates
+  if (meet(so, si) || meet(so, sg) || meet(ss, so) || meet(ss, sx) || meet(ss, si) || meet(ss, sg) ||
+      (routes && (meet(si, sg) || meet(si, sx) || meet(sg, sx))))
+    return EFFORT_ERR_ARG;
   call_scratch(h, &c, (char*)scratch, (int)n_tokens, top_k);
   DeviceGuard guard(h->dev);
   c.w13 = h->w13;

@@ -418,7 +418,8 @@ typedef enum { EFFORT_NORM_NONE = 0, EFFORT_NORM_RMS = 1, EFFORT_NORM_LAYER = 2 
  *   (but gate's 0) is at least dim (q_scales_stride: at least its blocks).
  *   Pointers are aligned to their element type.
  *   x_out and h_out may be the same array as x or y (same address, element
- *   size and stride); they overlap nothing else, nor one another.
+ *   size and stride).  Outputs that overlap inputs otherwise, or one another, are
+ *   refused.
  *   Runs on the current device, where all pointers have to live.
  */
 typedef struct {
@@ -468,7 +469,7 @@ effort_status_t effort_fp8_prepare(const void* q, const float* scales, int64_t i
  *   of 16 (what effort_block_norm writes for such a q_out), of which a row's
  *   bytes are read up to the next multiple of 16 (any value); x_scales: device
  *   fp32 [rows x ceil(in_dim / 128)].  out: [rows x out_dim] of out_dtype.
- *   0 <= rows <= EFFORT_MAX_ROWS.  out overlaps neither input.
+ *   0 <= rows <= EFFORT_MAX_ROWS.  An out that overlaps x or x_scales is refused.
  *   One kernel (two for 9 to 16 rows where in_dim > 196608); results do not vary
  *   from call to call.
  */
@@ -534,6 +535,8 @@ effort_status_t effort_moe_prepare(const effort_moe_weights_t* weights, void* st
  *   scratch: device memory of effort_moe_scratch_bytes(layer, n_tokens, top_k)
  *   bytes, 256-byte aligned, whose contents mean nothing before and after the
  *   call; calls that may overlap on the GPU bring scratch of their own.
+ *   out may lie over x, which has been read by then.  Any other overlap with what
+ *   the call writes is refused.
  *   A token whose logits hold NaN counts them as lowest; its gates are NaN.
  *   Precision: products of 16-bit and e4m3 values are exact, and sums are fp32
  *   (the matrix instructions' own over 64 or 128 terms).  With bfloat16 weights
