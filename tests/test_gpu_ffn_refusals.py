@@ -73,3 +73,41 @@ def test_norm_out_over_part_of_its_input_is_refused(E):
     ref = E.block_norm(a, b)
     r = E.block_norm(wide[:, :100], wide[:, 100:], x_out=wide[:, :100], h_out=wide[:, 100:])
     assert torch.equal(r.x, ref.x) and torch.equal(r.h, ref.h)
+
+
+# -- types of the matvec entry points, on live handles
+
+def test_matvecs_refuse_bfloat16_vectors(E):
+    W = (0.02 * randn(3, 256, 512)).half()
+    pm, ws = E.PreparedMatrix(W), E.Workspace(256, 512)
+    L, out = E.lib(), torch.empty(512, device="cuda")
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    for dtype, v, want in ((0, randn(4, 256), 0), (1, randn(4, 256).half(), 0), (2, randn(4, 256).bfloat16(), ARG),
+                           (3, randn(4, 256), ARG), (-1, randn(4, 256), ARG)):
+        p = ctypes.c_void_p(v.data_ptr())
+        o = ctypes.c_void_p(out.data_ptr())
+        assert L.effort_gemv_ex(pm._h, p, dtype, ctypes.c_float(0.5), o, None, None, None, stream) == want
+        assert L.effort_gemv_static(pm._h, p, dtype, ctypes.c_float(0.5), o, None, None, None, stream) == want
+        handles, zero = (ctypes.c_void_p * 1)(pm._h.value), (ctypes.c_int32 * 1)(0)
+        assert L.effort_gemv_batched(ws._h, handles, zero, zero, 1, p, dtype, (ctypes.c_float * 1)(0.5), o, None, None,
+                                     stream) == want
+        assert L.effort_dense_gemv(ws._h, ctypes.c_void_p(W.data_ptr()), 256, 512, p, dtype, o, stream) == want
+    torch.cuda.synchronize()
+    ws.close()
+    pm.close()
+
+
+# -- one dimension
+
+def test_one_dimension_with_every_argument(E):
+    x, y, g = randn(0, 500), randn(1, 500), randn(2, 500)
+    ref = E.block_norm(x[None], y[None], gate=g[None], post="layer", out_dtype=torch.bfloat16)
+    xo, ho = torch.empty(500, device="cuda"), torch.empty(500, device="cuda", dtype=torch.bfloat16)
+    r = E.block_norm(x, y, gate=g, post="layer", x_out=xo, h_out=ho)
+    assert r.x.data_ptr() == xo.data_ptr() and r.h.data_ptr() == ho.data_ptr()
+    assert torch.equal(xo, ref.x[0]) and torch.equal(ho, ref.h[0])
+    ref = E.block_norm(x[None], y[None], gate=g[None], post="layer", quantize=True)
+    r = E.block_norm(x, y, gate=g[None], post="layer", quantize=True)
+    assert r.q.shape == (500,) and r.scales.shape == (4,)
+    assert torch.equal(r.x, ref.x[0]) and torch.equal(r.scales, ref.scales[0])
+    assert torch.equal(r.q.view(torch.uint8), ref.q[0].view(torch.uint8))
