@@ -195,6 +195,7 @@ py::tuple moe_forward(uintptr_t handle, int64_t in_dim, int dev, const Tensor& x
   const auto type = x.scalar_type();
   const effort_dtype_t xdt = need_dtype(type, "x");
   const int64_t n = x.size(0);
+  const auto h = reinterpret_cast<effort_moe_t>(handle);
   Tensor ids, gates;
   if (mode == EFFORT_GATE_GIVEN) {
     ids = *ids_in;
@@ -206,28 +207,27 @@ py::tuple moe_forward(uintptr_t handle, int64_t in_dim, int dev, const Tensor& x
     };
     TORCH_CHECK_VALUE(good(ids, at::kInt) && good(gates, at::kFloat),
                       "ids and gates must be contiguous int32 and float32 [tokens, top_k] on cuda:", dev);
-  } else {
-    ids = make(n, top_k < 0 ? 0 : top_k, at::kInt, x);
-    gates = make(n, top_k < 0 ? 0 : top_k, at::kFloat, x);
   }
   if (out) need_rows(*out, "out", n, in_dim, dev);
   const auto ot = out ? out->scalar_type() : out_dtype ? *out_dtype : type;
   const effort_dtype_t odt = need_dtype(ot, "out_dtype");
+  // tokens and top_k are checked before anything of their size is made
+  const int32_t k = top_k < 0 ? 0 : top_k > INT32_MAX ? INT32_MAX : (int32_t)top_k;
+  size_t bytes = 0;
+  int st = n ? f_moe_scratch(h, n, k, &bytes) : 0;
+  if (st != 0) return py::make_tuple(st, py::none(), py::none(), py::none());
+  if (mode != EFFORT_GATE_GIVEN) {
+    ids = make(n, k, at::kInt, x);
+    gates = make(n, k, at::kFloat, x);
+  }
   Tensor o = out ? *out : make(n, in_dim, ot, x);
-  int st = 0;
   if (n) {
-    const auto h = reinterpret_cast<effort_moe_t>(handle);
-    size_t bytes = 0;
-    const int32_t k = top_k < 0 || top_k > INT32_MAX ? 0 : (int32_t)top_k;
-    st = f_moe_scratch(h, n, k, &bytes);
-    if (st == 0) {
-      // scratch of this call's own: the caching allocator keeps it apart from
-      // other streams' and other graphs' calls
-      const Tensor scratch = at::empty({(int64_t)bytes}, x.options().dtype(at::kByte));
-      st = f_moe_forward(h, x.data_ptr(), xdt, row_stride(x), n, k, (effort_gate_mode_t)mode, ids.data_ptr<int32_t>(),
-                         gates.data_ptr<float>(), o.data_ptr(), odt, row_stride(o), scratch.data_ptr(), bytes,
-                         c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream());
-    }
+    // scratch of this call's own: the caching allocator keeps it apart from
+    // other streams' and other graphs' calls
+    const Tensor scratch = at::empty({(int64_t)bytes}, x.options().dtype(at::kByte));
+    st = f_moe_forward(h, x.data_ptr(), xdt, row_stride(x), n, k, (effort_gate_mode_t)mode, ids.data_ptr<int32_t>(),
+                       gates.data_ptr<float>(), o.data_ptr(), odt, row_stride(o), scratch.data_ptr(), bytes,
+                       c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream());
   }
   return py::make_tuple(st, o, ids, gates);
 }

@@ -75,6 +75,24 @@ def test_norm_out_over_part_of_its_input_is_refused(E):
     assert torch.equal(r.x, ref.x) and torch.equal(r.h, ref.h)
 
 
+# -- sizes
+
+@pytest.mark.parametrize("k", [-1, 17, 2 ** 31, 2 ** 40])
+def test_top_k_is_checked_before_anything_is_made(E, layer, k):
+    held = torch.cuda.memory_reserved()
+    with pytest.raises(E.EffortError):
+        layer(randn(0, 4, 64), top_k=k)
+    assert torch.cuda.memory_reserved() <= held + (4 << 20)
+
+
+def test_too_many_tokens_are_refused_before_anything_is_made(E, layer):
+    x = torch.zeros(1, 64, device="cuda").expand(1 << 22, 64)
+    held = torch.cuda.memory_reserved()
+    with pytest.raises(E.EffortError):
+        layer(x, top_k=1)
+    assert torch.cuda.memory_reserved() <= held + (4 << 20)
+
+
 # -- types of the matvec entry points, on live handles
 
 def test_matvecs_refuse_bfloat16_vectors(E):
