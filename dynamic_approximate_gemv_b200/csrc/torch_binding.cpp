@@ -4,6 +4,7 @@
 // 2 to 4 us and the same steps in Python 8 to 13.  The entry points come as
 // addresses from the library that the Python side has loaded.
 #include <ATen/Functions.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
@@ -37,8 +38,20 @@ effort_dtype_t need_dtype(at::ScalarType t, const char* name) {
   return (effort_dtype_t)d;
 }
 
+// Tensors whose values do not lie in memory as they are: subclasses with a dispatch
+// of their own (fake tensors among them), vmap's and other transforms' wrappers,
+// lazily negated views.
+const c10::DispatchKeySet kWrapped({c10::DispatchKey::Python, c10::DispatchKey::FuncTorchBatched, c10::DispatchKey::FuncTorchGradWrapper,
+                                    c10::DispatchKey::Functionalize, c10::DispatchKey::Negative, c10::DispatchKey::Conjugate});
+void need_plain(const Tensor& t, const char* name) {
+  TORCH_CHECK_TYPE(!t.key_set().has_any(kWrapped), name, " must be a plain tensor, whose values lie in memory as they are");
+  TORCH_CHECK(!(t.requires_grad() && c10::GradMode::is_enabled()), name,
+              " asks for a gradient, but this operator has no backward pass: detach it, or call under torch.no_grad()");
+}
+
 // t is [rows, dim] on this device (any if negative), its rows' elements adjacent
 void need_rows(const Tensor& t, const char* name, int64_t rows, int64_t dim, int device) {
+  need_plain(t, name);
   TORCH_CHECK_VALUE(t.is_cuda(), name, " must be a CUDA tensor");
   TORCH_CHECK_VALUE(device < 0 || t.get_device() == device, name, " is on cuda:", (int)t.get_device(), ", expected cuda:", device);
   TORCH_CHECK_VALUE(t.dim() == 2 && (dim < 0 || t.size(1) == dim) && (rows < 0 || t.size(0) == rows), name, " must be [",
@@ -53,6 +66,7 @@ int64_t row_stride(const Tensor& t) { return t.size(0) > 1 ? t.stride(0) : t.siz
 
 const void* need_vector(const Opt& w, const char* name, int64_t dim, int device, std::optional<at::ScalarType>& type) {
   if (!w) return nullptr;
+  need_plain(*w, name);
   if (!type) {
     type = w->scalar_type();
     need_dtype(*type, name);
@@ -200,6 +214,8 @@ py::tuple moe_forward(uintptr_t handle, int64_t in_dim, int dev, const Tensor& x
   if (mode == EFFORT_GATE_GIVEN) {
     ids = *ids_in;
     gates = *gates_in;
+    need_plain(ids, "ids");
+    need_plain(gates, "gates");
     top_k = ids.dim() == 2 ? ids.size(1) : -1;
     auto good = [&](const Tensor& t, at::ScalarType want) {
       return t.is_cuda() && t.get_device() == dev && t.is_contiguous() && t.scalar_type() == want && t.dim() == 2 &&

@@ -7,6 +7,9 @@ binding this marshals arguments only: each call is one call of the C ABI on
 torch's current stream of the tensors' device, made by a compiled module
 (``csrc/torch_binding.cpp``) because the smallest calls' kernels are shorter than
 the same steps in Python.
+
+They are forward operators: an argument that asks for a gradient is refused with a
+RuntimeError unless gradients are off (``torch.no_grad()``).
 """
 import collections
 import ctypes

@@ -36,6 +36,42 @@ def layer(E):
                       router=randn(9, 4, 64))
 
 
+# -- gradients: there is no backward pass, so none is dropped in silence
+
+def test_inputs_that_want_gradients_are_refused(E, matrix, layer):
+    x, w = randn(0, 4, 64), randn(1, 64)
+    for call in (lambda t: E.block_norm(t), lambda t: E.block_norm(x, t), lambda t: E.block_norm(x, x, gate=t),
+                 lambda t: E.block_norm(x, pre_weight=t[0]), lambda t: E.block_norm(x, x, post="layer", post_bias=t[0]),
+                 lambda t: E.quantize_e4m3(t), lambda t: layer(t, top_k=1),
+                 lambda t: layer(x, ids=torch.zeros(4, 64, device="cuda", dtype=torch.int32)[:, :2].contiguous(),
+                                 gates=t[:, :2].contiguous())):
+        with pytest.raises(RuntimeError, match="gradient"):
+            call(x.clone().requires_grad_())
+        with torch.no_grad():
+            call(torch.nn.Parameter(x.clone()))
+        call(x)
+    q, s = E.quantize_e4m3(randn(2, 3, 256))
+    with pytest.raises(RuntimeError, match="gradient"):
+        matrix.matmul(q, s.clone().requires_grad_())
+    with torch.no_grad():
+        assert torch.equal(matrix.matmul(q, s.clone().requires_grad_()), matrix.matmul(q, s))
+
+
+def test_tensors_without_plain_storage_are_refused(E, layer):
+    x = randn(0, 4, 3, 64)
+    with pytest.raises((TypeError, ValueError)):
+        torch.vmap(lambda t: E.block_norm(t).h)(x)
+    with pytest.raises((TypeError, ValueError)):
+        torch.vmap(lambda t: layer(t, top_k=1)[0])(x)
+    with pytest.raises((TypeError, ValueError)):
+        E.block_norm(torch._neg_view(x[0]))
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    with FakeTensorMode():
+        fake = torch.empty(3, 64, device="cuda")
+    with pytest.raises((TypeError, ValueError)):
+        E.block_norm(fake)
+
+
 # -- outputs over inputs
 
 def test_product_out_over_its_inputs_is_refused(E, matrix):
