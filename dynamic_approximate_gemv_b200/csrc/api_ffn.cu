@@ -56,16 +56,21 @@ bool kind_ok(int k) { return k == EFFORT_NORM_NONE || k == EFFORT_NORM_RMS || k 
 struct Span {
   const void* p;
   int64_t rows, stride, width;
+  uintptr_t lo, hi;  // all of it; empty where p is null
+  Span(const void* p_, int64_t rows_, int64_t stride_, int64_t width_) : p(p_), rows(rows_), stride(stride_), width(width_) {
+    lo = hi = (uintptr_t)p;
+    uint64_t n;
+    if (p && (__builtin_mul_overflow((uint64_t)(rows - 1), (uint64_t)stride, &n) || __builtin_add_overflow(n, (uint64_t)width, &n) ||
+              __builtin_add_overflow(lo, n, &hi)))
+      hi = UINTPTR_MAX;
+  }
 };
 
-// Whether two arrays have a byte in common.
-bool meet(const Span& a, const Span& b) {
-  if (!a.p || !b.p) return false;
-  using Wide = __int128;
-  const Wide a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p, d = b0 - a0;
-  if (a0 + (Wide)(a.rows - 1) * a.stride + a.width <= b0 || b0 + (Wide)(b.rows - 1) * b.stride + b.width <= a0) return false;
+// Whether two arrays whose ranges overlap have a byte in common.
+bool rows_meet(const Span& a, const Span& b) {
   if (a.rows == 1 && b.rows == 1) return true;
-  const Wide sa = a.rows > 1 ? a.stride : b.stride, sb = b.rows > 1 ? b.stride : a.stride;
+  using Wide = __int128;
+  const Wide d = (Wide)b.lo - (Wide)a.lo, sa = a.rows > 1 ? a.stride : b.stride, sb = b.rows > 1 ? b.stride : a.stride;
   if (sa == sb) {
     // row i of a, i + k of b: k's least value with d + k s > -b.width, and in b
     const Wide num = -(Wide)b.width - d;
@@ -81,6 +86,7 @@ bool meet(const Span& a, const Span& b) {
   }
   return false;
 }
+inline bool meet(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi && rows_meet(a, b); }
 
 effort_status_t device_sms(int* sms) {
   int dev = 0;
