@@ -452,8 +452,10 @@ def measure_chain(E, dev, layers=32, dims=(4096, 1024, 14336), effort=0.25, keep
             L[n].close()
     return {"workload": f"{layers} layers of q {dims[0]}x{dims[0]}, k/v {dims[0]}x{dims[1]}, o {dims[0]}x{dims[0]}, "
                         f"w1/w3 {dims[0]}x{dims[2]}, w2 {dims[2]}x{dims[0]} fp16 N(0,0.02^2), keep {keep}, "
-                        f"effort {effort}; {7 * layers} dependent matvecs per token, RMS-normalised inputs",
-            "us_per_token": us, "matvecs_per_token": 7 * layers, "us_per_matvec": us / (7 * layers),
+                        f"effort {effort}; {7 * layers} dependent matvecs per token, joined by {5 * layers} RMS norms (the "
+                        f"library's, one kernel each) and {layers} elementwise products, all in the token's time",
+            "us_per_token": us, "matvecs_per_token": 7 * layers, "norms_per_token": 5 * layers,
+            "us_per_matvec": us / (7 * layers),  # with its share of the norms and products
             "dense_roofline_us_per_token_measured_peak": dense_bytes / (hbm_peak()[0] * 1e9) * 1e6,
             "prepared_bytes": storage,
             "per_matrix_schedule": {"efforts": CHAIN_EQUALIZER, "parameter_weighted_mean_effort": eq_mean,

@@ -343,10 +343,21 @@ cudaError_t launch_fp8_matmul(const TileMat& w, const float* ws, int I, int O, c
                               const float* xs, int64_t xsstride, int64_t rows, int odt, void* out, int64_t ostride,
                               cudaStream_t s) {
   // Few rows stream through registers, with the least to set up: up to 8, and
-  // up to 16 of small matrices (16x1000x500: 2.9 against 4.1 us; 13x14336x4096:
-  // 24 against 15).  A wide and large matrix fills the tensor cores' tiles at
-  // once (8x4096x14336: 13.4 against 15.9 us; one row 13.2 against 13.8; but
-  // 8x14336x4096 15.2 against 13.5, 4x4096x4096 8.5 against 5.4).
+  // up to 16 of small matrices.  A wide and large matrix fills the tensor cores'
+  // tiles at once.  Measured, stream / tensor cores in us, in x out:
+  //   rows           2           8           9           16
+  //   512 x 512      1.9 / 2.9   2.1 / 3.0   2.6 / 3.0   2.8 / 3.2
+  //   1024 x 2048    2.8 / 3.9   3.0 / 4.0   3.0 / 4.1   3.3 / 4.2
+  //   4096 x 1024    3.1 / 5.8   3.6 / 6.3   5.8 / 6.3   6.7 / 6.4
+  //   2048 x 4096    3.7 / 6.5   4.0 / 6.7   4.9 / 6.7   5.4 / 6.7
+  //   4096 x 4096    5.2 / 8.3   5.7 / 8.5   7.7 / 8.5   8.7 / 8.6
+  //   4096 x 8192    8.4 / 10.5  9.3 / 10.7  10.1 / 10.6 11.3 / 10.7
+  //   2048 x 16384   9.2 / 9.0   10.3 / 9.4  10.9 / 9.5  12.5 / 9.6
+  //   4096 x 14336   13.2 / 13.0 15.1 / 13.2 17.0 / 13.2 19.6 / 13.5
+  //   14336 x 4096   11.4 / 14.5 13.2 / 14.7 21.7 / 14.7 24.8 / 14.7
+  //   8192 x 28672   41.6 / 43.0 44.3 / 43.1 55.5 / 43.1 64.4 / 43.7
+  // So the rule gives up to 2 us away where 9 to 12 rows meet 4 to 32 M weights, and
+  // where 2 to 8 rows meet 32 M that are just twice as wide as long.
   const long long size = (long long)I * O;
   const bool wide = rows > 1 && O >= 2 * I && size >= 32ll << 20;
   if (wide || rows > kFewRowsMax || (rows > 8 && size > 2ll << 20))

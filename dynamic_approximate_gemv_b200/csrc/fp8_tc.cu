@@ -659,6 +659,14 @@ cudaError_t launch_fp8_tc(const TileMat& w, const float* ws, int I, int O, const
   if (rows <= 16) GO(false, 128, 16);
   if (rows <= 32) GO(false, 128, 32);
   if (rows <= 64) GO(false, 128, 64);
+  // Tiles of 128 x 128 split their K over a cluster where they are few; 128 x 256
+  // reads less and adds more at once, but goes in whole tiles, 148 at a time.
+  // Measured, 128 x 128 / 128 x 256 in us, by tiles of 128 x 256:
+  //   tiles       16        64         80         112        168        224        280        448        512
+  //   K = 4096    11.0/23.7 18.7/26.0  29.0/27.1  31.8/28.9  42.5/49.4  54.4/49.5  57.4/51.5  90.7/91.8  93.5/90.8
+  //   K = 1024    5.8/9.0   7.2/9.4    11.2/10.5  11.1/11.1  14.6/19.4  17.8/19.1  19.8/21.4  30.0/35.6  30.2/35.6
+  // From 149 tiles on, just behind a whole round, the wide shape is up to a third
+  // slower, and at a short K up to a fifth throughout; the rule does not see that.
   if ((long long)cdiv(O, 256) * cdiv(rows, 128) < 100) GO(true, 128, 128);
   GO(true, 128, 256);
 #undef GO

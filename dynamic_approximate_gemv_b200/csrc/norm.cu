@@ -4,10 +4,10 @@
 //   u = post(y);  x' = a x + b g u;  h = pre(x');  s = max|h| over 128 / 448, q = h / s
 //
 // Bound by its bytes: every input is read once and every output written once,
-// and a row stays in its block's registers in between.  One block per row,
-// rows in turn; the next row's values are on their way (as they are stored)
-// while a row's sums are joined.  A warp owns whole blocks of 128 columns, so that a
-// block's maximum needs shuffles only.  A mean of squares is taken of the
+// and a row stays in its block's registers in between.  One block per row, rows in
+// turn: loaded as they are needed where there are few (k_block_norm), two rows ahead
+// through shared memory where there are many (k_block_norm_rows).  A warp owns whole
+// blocks of 128 columns, so that a block's maximum needs shuffles only.  A mean of squares is taken of the
 // differences from the mean, in a second pass over the registers.
 #include <atomic>
 #include <type_traits>

@@ -411,7 +411,9 @@ typedef enum { EFFORT_NORM_NONE = 0, EFFORT_NORM_RMS = 1, EFFORT_NORM_LAYER = 2 
  *     pass); a block of zeros (or one whose scale underflows to zero) has scale 0
  *     and q 0.  A block that holds inf or NaN has scale inf or NaN.
  *     This is the form effort_fp8_matmul takes.
- * h is computed from x' before x' is rounded.
+ * h is computed from x' before x' is rounded.  Squares are fp32: a row whose values
+ * exceed about 1e19 has an infinite mean square and so h = bias (0 without one), and
+ * values below about 1e-19 count as nothing beside eps.
  *   dtype: of x, y, gate and x_out.  weight_dtype: of all weights and biases [dim].
  *   gate: nullable; gate_stride 0 uses one row for all rows.
  *   1 <= dim <= EFFORT_MAX_IN_DIM, 0 <= rows <= EFFORT_MAX_ROWS; every stride
@@ -469,6 +471,8 @@ effort_status_t effort_fp8_prepare(const void* q, const float* scales, int64_t i
  *   of 16 (what effort_block_norm writes for such a q_out), of which a row's
  *   bytes are read up to the next multiple of 16 (any value); x_scales: device
  *   fp32 [rows x ceil(in_dim / 128)].  out: [rows x out_dim] of out_dtype.
+ *   A block's sum meets its two scales one after the other, or (on the tensor cores)
+ *   their product, in fp32: where that leaves fp32's range, so does the result.
  *   0 <= rows <= EFFORT_MAX_ROWS.  An out that overlaps x or x_scales is refused.
  *   One kernel (two for 9 to 16 rows where in_dim > 196608); results do not vary
  *   from call to call.
@@ -497,7 +501,8 @@ effort_status_t effort_fp8_destroy(effort_fp8_t m);
  *   All are read during the call only (the stream is synchronised before
  *   returning); the handle keeps its own copies.
  *   1 <= n_experts <= EFFORT_MAX_EXPERTS, 1 <= in_dim, hidden_dim <= EFFORT_MAX_IN_DIM.
- *   Returns EFFORT_ERR_NONFINITE if a weight or scale is inf or NaN.
+ *   Returns EFFORT_ERR_NONFINITE if an expert's weight or scale is inf or NaN (the
+ *   router's values are not checked).
  */
 #define EFFORT_MAX_EXPERTS 256
 #define EFFORT_MAX_TOKENS 256   /* n_tokens of one call */
