@@ -268,8 +268,9 @@ using MoeShape = StreamShape<ROWS, (WK == kWE4M3 ? 128 : 64) * 2 * PARTS, 64, kM
 // lower by as much as some column of the block, or some input, stands out.
 __device__ __forceinline__ void hidden_scale(double xnorm, double2 n, float* up, float* down) {
   const double b = xnorm * n.x * (xnorm * n.y);
-  // b < 2^k; the values themselves are fp32 (inf and NaN end up somewhere)
-  const int k = max(-111, min((__double2hiint(b) >> 20 & 0x7ff) - 1022, 128));
+  // b < 2^k, at least 2^-96 as in pow2_scale; the values themselves are fp32 (inf and
+  // NaN end up somewhere)
+  const int k = max(-96, min((__double2hiint(b) >> 20 & 0x7ff) - 1022, 128));
   *up = __uint_as_float((uint32_t)(127 + 15 - k) << 23);
   *down = __uint_as_float((uint32_t)(127 - 15 + k) << 23);
 }
@@ -429,14 +430,20 @@ __global__ void __launch_bounds__(MoeShape<WK, PARTS, ROWS>::kThreads, 1) k_moe_
     for (int kb = G.kb0 + wk; kb < G.kb1; kb += kw) {
       const uint32_t at = ring.wait(smem, warp, c.hook, [&]() { pc.u = u1; });
       uint32_t b[PARTS][NT][KS][2];
-      float sc[NT][2][2];  // the scales of column 2 q + e and the tile's rows g, g + 8: x's is a power of two
+      // the scales of column 2 q + e and the tile's rows g, g + 8: x's power of two times
+      // the weights', as far as it is above 1, and before that what is below (so
+      // that no product of two of the three leaves fp32's range where all three do not)
+      constexpr bool kLess = SCALED && WK == kWE4M3;
+      float sc[NT][2][2], less[NT][2];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         act_load<PARTS, NT, KS>(at + S::kActAt + (8 * j + g) * S::kRowPitch, q, 8 * j + g < G.count, b, j);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {  // of the columns this lane has sums of
           const int r = 8 * j + 2 * q + e;
-          sc[j][e][0] = sc[j][e][1] = SCALED && r < G.count ? lds_float(at + S::kActAt + r * S::kRowPitch + KE * 2 * PARTS) : 1.0f;
+          const float sx = SCALED && r < G.count ? lds_float(at + S::kActAt + r * S::kRowPitch + KE * 2 * PARTS) : 1.0f;
+          less[j][e] = kLess ? fminf(sx, 1.0f) : 1.0f;
+          sc[j][e][0] = sc[j][e][1] = kLess ? fmaxf(sx, 1.0f) : sx;
         }
       }
       if constexpr (WK == kWE4M3) {
@@ -460,7 +467,7 @@ __global__ void __launch_bounds__(MoeShape<WK, PARTS, ROWS>::kThreads, 1) k_moe_
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[m][j][e] = fmaf(d[j][e], sc[j][e & 1][e >> 1], acc[m][j][e]);
+          for (int e = 0; e < 4; ++e) acc[m][j][e] = fmaf(d[j][e] * less[j][e & 1], sc[j][e & 1][e >> 1], acc[m][j][e]);
       }
       __syncwarp();  // every lane has read the stage
       ask();

@@ -411,9 +411,10 @@ typedef enum { EFFORT_NORM_NONE = 0, EFFORT_NORM_RMS = 1, EFFORT_NORM_LAYER = 2 
  *     pass); a block of zeros (or one whose scale underflows to zero) has scale 0
  *     and q 0.  A block that holds inf or NaN has scale inf or NaN.
  *     This is the form effort_fp8_matmul takes.
- * h is computed from x' before x' is rounded.  Squares are fp32: a row whose values
- * exceed about 1e19 has an infinite mean square and so h = bias (0 without one), and
- * values below about 1e-19 count as nothing beside eps.
+ * h is computed from x' before x' is rounded.  Squares and their sum are fp32: a row
+ * whose sum of squares exceeds fp32 (values of 3e17 throughout 4096 columns) gives
+ * h = bias (0 without one), and squares below fp32's normal numbers (values under
+ * 1e-19) lose bits, which shows where eps is as small.
  *   dtype: of x, y, gate and x_out.  weight_dtype: of all weights and biases [dim].
  *   gate: nullable; gate_stride 0 uses one row for all rows.
  *   1 <= dim <= EFFORT_MAX_IN_DIM, 0 <= rows <= EFFORT_MAX_ROWS; every stride
@@ -555,7 +556,7 @@ effort_status_t effort_moe_prepare(const effort_moe_weights_t* weights, void* st
  *       block's largest |x| (or 2^-97);
  *     hidden activations: two parts; one where out is bfloat16, unless column
  *       norms of w1 or w3 differ by more than 32 times within a K block; the bound
- *       is |x|^2 times the largest column norms of w1 and w3 over the block.
+ *       is |x|^2 times the largest column norms of w1 and w3 over the block (or 2^-96).
  *   The router's logits are fp32 sums: experts whose logits differ by less than
  *   their rounding may change places.
  *   Results do not vary from call to call.

@@ -13,8 +13,8 @@ hold 22 bits (error 2^-23) down to 2^-36 / 2^14 = 2^-50 M.  Three bfloat16
 parts hold 24 bits and more (error 2^-26).
 
 Hidden activations.  With binary16 and e4m3 weights likewise, with the bound
-B = |x|^2 |w1| |w3| (norms of x and of the largest columns of the K block) in M's
-place; a bfloat16 out takes one part, 11 bits (error 2^-11, and 2^-39 B), unless
+B = |x|^2 |w1| |w3| (norms of x and of the largest columns of the K block; 2^-96 if
+that is larger) in M's place; a bfloat16 out takes one part, 11 bits (error 2^-11, and 2^-39 B), unless
 norms of columns differ by more than 32 times within a K block.  With bfloat16
 weights two parts (16-bit out; error 2^-17), or three.
 
@@ -78,7 +78,7 @@ def moe(x, w1, w3, w2, ids, gates, out_dtype, kind):
         else:
             bound = xt.square().sum(1, keepdim=True) * block_max(w1[j].norm(dim=0)[None], ke) * block_max(w3[j].norm(dim=0)[None], ke)
             few = out_dtype == torch.bfloat16 and not any(spread(w[k], ke) for w in (w1, w3) for k in range(e))
-            dh = dh + (h.abs() + dh) * 2.0 ** (-11 if few else -23) + bound.clamp(min=2.0 ** -111) * 2.0 ** (-39 if few else -50)
+            dh = dh + (h.abs() + dh) * 2.0 ** (-11 if few else -23) + bound.clamp(min=2.0 ** -96) * 2.0 ** (-39 if few else -50)
         g = gates[t, slot].double()[:, None]
         y = h @ w2[j]
         dy = dh @ w2[j].abs() + (h.abs() + dh) @ w2[j].abs() * steps(f)
