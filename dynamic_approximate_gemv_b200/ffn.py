@@ -127,13 +127,13 @@ class Fp8Matrix:
             _check(lib().effort_fp8_prepare(q.data_ptr(), scales.data_ptr(), self.in_dim, self.out_dim,
                                             _stream(q.device), ctypes.byref(h)), "effort_fp8_prepare")
         self._h = h
-        self._index, self._call = q.device.index, _binding().fp8_matmul
+        self._handle, self._index, self._call = h.value, q.device.index, _binding().fp8_matmul
 
     def matmul(self, x, x_scales, out=None, out_dtype=torch.bfloat16):
         """out[r, n] = sum_k x_scales[r, k // 128] x[r, k] w[k, n].  x: e4m3
         [rows, in_dim] whose rows start on 16-byte boundaries, x_scales: float32
         [rows, ceil(in_dim / 128)], both as block_norm(quantize=True) gives them."""
-        status, out = self._call(self._h.value, self.in_dim, self.out_dim, self._index, x, x_scales, out, out_dtype)
+        status, out = self._call(self._handle, self.in_dim, self.out_dim, self._index, x, x_scales, out, out_dtype)
         if status:
             raise EffortError(status, "effort_fp8_matmul")
         return out
@@ -147,7 +147,7 @@ class Fp8Matrix:
     def close(self):
         if getattr(self, "_h", None):
             lib().effort_fp8_destroy(self._h)
-            self._h = None
+            self._h, self._handle = None, 0
 
     def __del__(self):
         try:
@@ -200,7 +200,7 @@ class MoeLayer:
             _check(lib().effort_moe_prepare(ctypes.byref(a), _stream(w1.device), ctypes.byref(h)),
                    "effort_moe_prepare")
         self._h = h
-        self._index, self._call = w1.device.index, _binding().moe_forward
+        self._handle, self._index, self._call = h.value, w1.device.index, _binding().moe_forward
 
     def __call__(self, x, top_k=None, gate_mode="softmax_of_top", ids=None, gates=None, out=None, out_dtype=None):
         """x: [tokens, in_dim] (float32, float16 or bfloat16), at most MAX_TOKENS.
@@ -219,7 +219,7 @@ class MoeLayer:
             if not self._router:
                 raise ValueError("this layer has no router: give ids and gates")
             mode = _GATE[gate_mode]
-        status, out, ids, gates = self._call(self._h.value, self.in_dim, self._index, x, top_k, mode, ids, gates, out,
+        status, out, ids, gates = self._call(self._handle, self.in_dim, self._index, x, top_k, mode, ids, gates, out,
                                              out_dtype)
         if status:
             raise EffortError(status, "effort_moe_forward")
@@ -234,7 +234,7 @@ class MoeLayer:
     def close(self):
         if getattr(self, "_h", None):
             lib().effort_moe_destroy(self._h)
-            self._h = None
+            self._h, self._handle = None, 0
 
     def __del__(self):
         try:

@@ -129,6 +129,21 @@ def test_too_many_tokens_are_refused_before_anything_is_made(E, layer):
     assert torch.cuda.memory_reserved() <= held + (4 << 20)
 
 
+# -- closed handles
+
+def test_closed_handles_are_refused(E):
+    m = E.Fp8Matrix(*R.quantise_weights(0.05 * randn(1, 256, 128)))
+    layer = E.MoeLayer(*(0.05 * randn(k, 2, 32, 32).half() for k in range(3)), router=randn(9, 2, 32))
+    q, s = E.quantize_e4m3(randn(2, 3, 256))
+    for h in (m, layer):
+        h.close()
+        h.close()
+    for call in (lambda: m.matmul(q, s), m.info, lambda: layer(randn(0, 4, 32), top_k=1), layer.info):
+        with pytest.raises(E.EffortError) as e:
+            call()
+        assert e.value.status == ARG
+
+
 # -- types of the matvec entry points, on live handles
 
 def test_matvecs_refuse_bfloat16_vectors(E):
